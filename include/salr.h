@@ -333,6 +333,75 @@ SALR_API int salr_residual_adapter(const void* W, salr_handle h, int64_t r, cons
                                    int64_t l, int q, void* A_out, void* B_out, void* sigma_out,
                                    void* stream);
 
+/*
+ * salr_adamw - one AdamW step over many tensors (the adapters of a model) at once.
+ *
+ * Defined by: the adapters, the residual adapter among them, are what fine-tuning trains
+ * (technical summary, Methodology 2 and 3); AdamW is Adam with decoupled weight decay
+ * (Loshchilov and Hutter, 2019).  For every element, with t = step[0] + 1:
+ *
+ *     g' = grad_scale g
+ *     m  = beta1 m + (1 - beta1) g'         v = beta2 v + (1 - beta2) g'^2
+ *     p  = (1 - lr weight_decay) p - lr / (1 - beta1^t) m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+ *
+ * in fp32, each operation rounded to nearest on its own.  The step advances step[0] by one.
+ *
+ * tensors  host array of `count` entries, read before the call returns.  An entry with
+ *          n == 0 or grad == NULL is skipped (its moments stay as they are; the one step
+ *          count still advances).  The memory of two entries must not overlap.
+ *   param          device, n values of param_type, contiguous; updated.
+ *   grad           device, n values of grad_type; read only.
+ *   master         device, n fp32, 16-byte aligned: with config.master, the value p that
+ *                  the step updates; param then receives its bf16 rounding.  Else ignored.
+ *   exp_avg, exp_avg_sq  device, 16-byte aligned: n fp32 each (state_bits 32: m and v), or
+ *                  n e4m3 codes each, rounded up to a multiple of 256 (state_bits 8).
+ *   exp_avg_scale, exp_avg_sq_scale  state_bits 8: device, one fp32 per 256 elements.
+ *                  Elements 256 j .. 256 j + 255 of the tensor hold m = code * scale[j] in
+ *                  exp_avg and sqrt(v) = code * scale[j] in exp_avg_sq, scale[j] = the
+ *                  block's largest finite magnitude / 448.  A positive sqrt(v) is held as
+ *                  at least 2^-9 scale; a block below 2^-100 is held as zeros; a value that
+ *                  is not finite is held as NaN.  All bytes zero is the initial state.
+ * config   host, read before the call returns.
+ *   step           device, two int64, 8-byte aligned: the number of steps done, and a zero
+ *                  that the call uses and leaves zero.
+ *   lr_dev         device, one fp32 that takes the place of lr, or NULL.
+ *   grad_scale     device, one fp32, or NULL for 1.
+ *
+ * param and grad need the alignment of their type only; tensors whose param and grad are
+ * 16-byte aligned are read by 16-byte loads.  One kernel launch per 448 tensors; nothing is
+ * allocated or kept, so a captured step can be replayed: it then reads step, lr_dev and
+ * grad_scale as they are at the replay.  Two steps over the same tensors or the same `step`
+ * must be ordered on one stream.
+ *
+ * SALR_ERR_INVALID: a NULL array, config, step or needed pointer, n or count < 0, an unknown
+ * type or state_bits, master with fp32 param, beta1 or beta2 outside [0, 1), a negative or
+ * non-finite eps, a non-finite lr or weight_decay.  SALR_ERR_UNSUPPORTED: alignment as
+ * above, n > 2^38.
+ */
+enum { SALR_BF16 = 0, SALR_FP32 = 1 };
+typedef struct {
+  void* param;
+  const void* grad;
+  float* master;
+  void* exp_avg;
+  void* exp_avg_sq;
+  float* exp_avg_scale;
+  float* exp_avg_sq_scale;
+  int64_t n;
+} salr_adamw_tensor;
+typedef struct {
+  double lr, beta1, beta2, eps, weight_decay;
+  const void* lr_dev;
+  const void* grad_scale;
+  void* step;
+  int32_t param_type; /* SALR_BF16 or SALR_FP32 */
+  int32_t grad_type;
+  int32_t state_bits; /* 32 or 8 */
+  int32_t master;     /* 1: fp32 master copies of bf16 parameters */
+} salr_adamw_config;
+SALR_API int salr_adamw(const salr_adamw_tensor* tensors, int64_t count,
+                        const salr_adamw_config* config, void* stream);
+
 /* salr_sync_status - synchronise `stream`, return the first device-side error recorded
  * for this handle since the last call (SALR_OK if none) and clear it. */
 SALR_API int salr_sync_status(salr_handle h, void* stream);

@@ -7,6 +7,7 @@ library, the first call does (and fails loudly if it has not been built).
 """
 from .binding import (SIGNATURES, SalrError, SalrPlan, Weight, encode, linear, linear_host,
                       load, load_library, plan, residual_adapter, status_string)
+from .optim import AdamW
 
-__all__ = ["SIGNATURES", "SalrError", "SalrPlan", "Weight", "encode", "linear", "linear_host",
+__all__ = ["AdamW", "SIGNATURES", "SalrError", "SalrPlan", "Weight", "encode", "linear", "linear_host",
            "load", "load_library", "plan", "residual_adapter", "status_string"]

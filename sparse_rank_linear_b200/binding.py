@@ -34,6 +34,21 @@ class SalrPlan(ctypes.Structure):
                 ("whole_tiles", ctypes.c_int32), ("splits", ctypes.c_int32),
                 ("split_sum_bytes", ctypes.c_int64), ("dense_scratch_bytes", ctypes.c_int64),
                 ("group_rows", ctypes.c_int32)]
+
+
+class AdamwTensor(ctypes.Structure):
+    """salr_adamw_tensor of include/salr.h."""
+    _fields_ = [("param", _P), ("grad", _P), ("master", _P), ("exp_avg", _P), ("exp_avg_sq", _P),
+                ("exp_avg_scale", _P), ("exp_avg_sq_scale", _P), ("n", _I64)]
+
+
+class AdamwConfig(ctypes.Structure):
+    """salr_adamw_config of include/salr.h."""
+    _fields_ = ([(f, ctypes.c_double) for f in ("lr", "beta1", "beta2", "eps", "weight_decay")] +
+                [(f, _P) for f in ("lr_dev", "grad_scale", "step")] +
+                [(f, ctypes.c_int32) for f in ("param_type", "grad_type", "state_bits", "master")])
+
+
 SIGNATURES = {
     "salr_encode": (_I, [_P, _I64, _I64, _F, _P, ctypes.POINTER(_P)]),
     "salr_decode": (_I, [_P, _P, _P]),
@@ -50,6 +65,7 @@ SIGNATURES = {
     "salr_load": (_I, [_P, _I64, _P, ctypes.POINTER(_P)]),
     "salr_residual_adapter": (_I, [_P, _P, _I64, _P, _I64, _I, _P, _P, _P, _P]),
     "salr_linear_plan": (_I, [_I64, _I64, _I64, _I64, ctypes.c_int32, ctypes.POINTER(SalrPlan)]),
+    "salr_adamw": (_I, [ctypes.POINTER(AdamwTensor), _I64, ctypes.POINTER(AdamwConfig), _P]),
     "salr_sync_status": (_I, [_P, _P]),
     "salr_status_string": (ctypes.c_char_p, [_I]),
 }

@@ -14,9 +14,9 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libsalr.so")
-SOURCES = ["salr_api.cu"]
+SOURCES = ["salr_api.cu", "salr_adamw.cu"]
 HEADERS = ["sm100.cuh", "salr_block.cuh", "salr_decode.cuh", "salr_codec.cuh", "salr_prefill.cuh",
-           "salr_stream.cuh", "salr_svd.cuh"]
+           "salr_stream.cuh", "salr_svd.cuh", "salr_host.h", "salr_adamw.cuh"]
 
 
 def nvcc_path() -> str:
@@ -28,7 +28,7 @@ def nvcc_path() -> str:
 
 def command(out: str = LIB, extra=()) -> list:
     return [nvcc_path(), "-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo",
-            "-std=c++17", "-shared", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
+            "-std=c++17", "-shared", "--threads", "0", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
             "-I", os.path.join(ROOT, "include"), *extra,
             *[os.path.join(CSRC, s) for s in SOURCES], "-o", out, "-cudart", "static"]
 

@@ -1,0 +1,265 @@
+// salr_adamw.cuh - one AdamW step over many tensors in one launch.
+//
+// For every element, with t the number of this step and g' = grad_scale g:
+//   m <- b1 m + (1 - b1) g'          v <- b2 v + (1 - b2) g'^2
+//   p <- (1 - lr wd) p - lr / (1 - b1^t) * m / (sqrt(v) / sqrt(1 - b2^t) + eps)
+// Every fp32 operation is rounded on its own (no contraction into fused multiply-adds), so
+// that the 8-bit codes below do not depend on how a compiler groups the operations.
+//
+// 8-bit moments: blocks of 256 consecutive elements of a tensor hold m and r = sqrt(v) as
+// e4m3 values x / scale with one fp32 scale = max|x| / 448 per block.  r rather than v: its
+// range over a block is half as many binades, and e4m3 has 17 of them (2^-9 .. 448).  A
+// positive r never becomes zero (it is held as at least 2^-9 scale): a zero there would
+// divide m by eps alone.  A block whose largest magnitude is below 2^-100 is held as zeros
+// (448 / max would leave fp32's normal range).  Non-finite values are held as NaN and do
+// not enter the block's maximum.
+//
+// Bound: HBM.  An element moves 28 bytes with bf16 parameters and gradients, fp32 moments
+// and master copies, and 10 bytes with 8-bit moments and no master copies, so the work is
+// laid out for loads in flight: one warp per 256-element block, 8 elements a thread, every
+// load of a block issued before the first use (up to 112 bytes a thread).  The tensor
+// table travels in the kernel's parameters: no copy, nothing to keep alive, one launch.
+#pragma once
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+
+namespace salr {
+
+constexpr int kAdamBlock = 256;    // elements per warp pass and per 8-bit scale
+constexpr int kAdamThreads = 256;  // 8 warps
+constexpr float kE4m3Max = 448.f;
+constexpr float kAdamFlush = 7.888609052210118e-31f;  // 2^-100
+
+struct AdamTensor {  // as salr_adamw_tensor
+  void* param;
+  const void* grad;
+  float* master;
+  void* m;
+  void* v;
+  float* m_scale;
+  float* v_scale;
+  int64_t n;
+};
+
+struct AdamScalars {
+  double lr, beta1, beta2, weight_decay;
+  float eps, b1, ob1, b2, ob2;  // b1 = (float)beta1, ob1 = (float)(1 - beta1), ...
+  const float* lr_dev;          // replaces lr when given
+  const float* grad_scale;      // NULL: 1
+  long long* step;              // [0] steps done, [1] CTAs done (zero between launches)
+  int last;                     // this launch ends the step: it advances step[0]
+};
+
+// Table of one launch: tensor i covers the 256-element blocks start[i] .. start[i + 1) - 1.
+template <int MAXT>
+struct AdamTable {
+  AdamScalars s;
+  int count;
+  int start[MAXT + 1];
+  AdamTensor t[MAXT];
+};
+
+__device__ __forceinline__ double adam_pow(double b, long long t) {
+  double r = 1.0;
+  for (; t > 0; t >>= 1, b *= b)
+    if (t & 1) r *= b;
+  return r;
+}
+
+// 8 consecutive values at element i of p, as fp32 (p + i is 16-byte aligned).
+__device__ __forceinline__ void adam_load8(const float* p, int64_t i, float (&x)[8]) {
+  const float4 a = __ldcs(reinterpret_cast<const float4*>(p + i));
+  const float4 b = __ldcs(reinterpret_cast<const float4*>(p + i) + 1);
+  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+  x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+}
+__device__ __forceinline__ void adam_load8(const __nv_bfloat16* p, int64_t i, float (&x)[8]) {
+  const uint4 a = __ldcs(reinterpret_cast<const uint4*>(p + i));
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    x[2 * k] = __uint_as_float(w[k] << 16);
+    x[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void adam_store8(float* p, int64_t i, const float (&x)[8]) {
+  __stcs(reinterpret_cast<float4*>(p + i), make_float4(x[0], x[1], x[2], x[3]));
+  __stcs(reinterpret_cast<float4*>(p + i) + 1, make_float4(x[4], x[5], x[6], x[7]));
+}
+__device__ __forceinline__ void adam_store8(__nv_bfloat16* p, int64_t i, const float (&x)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * k], x[2 * k + 1]);
+    w[k] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  __stcs(reinterpret_cast<uint4*>(p + i), make_uint4(w[0], w[1], w[2], w[3]));
+}
+__device__ __forceinline__ float adam_float(float x) { return x; }
+__device__ __forceinline__ float adam_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ void adam_set(float* p, float x) { *p = x; }
+__device__ __forceinline__ void adam_set(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
+
+// The `cnt` (1 .. 8) values from element i on, by vectors where allowed; the rest are 0.
+template <typename T>
+__device__ __forceinline__ void adam_get(const T* p, int64_t i, int cnt, bool vec, float (&x)[8]) {
+  if (vec && cnt == 8) {
+    adam_load8(p, i, x);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[k] = k < cnt ? adam_float(p[i + k]) : 0.f;
+  }
+}
+template <typename T>
+__device__ __forceinline__ void adam_put(T* p, int64_t i, int cnt, bool vec, const float (&x)[8]) {
+  if (vec && cnt == 8) {
+    adam_store8(p, i, x);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k < cnt) adam_set(p + i + k, x[k]);
+  }
+}
+
+__device__ __forceinline__ float e4m3_value(uint32_t code) {
+  const __half_raw h = __nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(code), __NV_E4M3);
+  return __half2float(__half(h));
+}
+
+// The thread's 8 codes at element i.  Codes start 8-byte aligned in every tensor, and the
+// caller pads a tensor's codes to whole blocks.
+__device__ __forceinline__ uint2 adam_codes(const void* p, int64_t i) {
+  return __ldcs(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p) + i));
+}
+__device__ __forceinline__ void adam_decode(uint2 c, float scale, float (&x)[8]) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    x[k] = __fmul_rn(e4m3_value(((k < 4 ? c.x : c.y) >> (8 * (k & 3))) & 255u), scale);
+}
+
+// Store x (8 values a thread, the warp's block) as e4m3 codes at element i and the block's
+// scale at *sp.  All 32 lanes call it together.
+template <bool POSITIVE>
+__device__ __forceinline__ void adam_encode(const float (&x)[8], void* codes, int64_t i, float* sp,
+                                            int lane) {
+  float top = 0.f;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const float a = fabsf(x[k]);
+    top = a <= 3.402823466e38f ? fmaxf(top, a) : top;  // finite values only
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const bool live = top >= kAdamFlush;
+  const float inv = live ? __fdiv_rn(kE4m3Max, top) : 0.f;
+  uint32_t w[2] = {0, 0};
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const float y = __fmul_rn(x[k], inv);
+    uint32_t c = __nv_cvt_float_to_fp8(y, __NV_SATFINITE, __NV_E4M3);
+    if (POSITIVE && y > 0.f && c == 0) c = 1;
+    if (!(fabsf(x[k]) <= 3.402823466e38f)) c = 0x7f;  // NaN
+    w[k >> 2] |= c << (8 * (k & 3));
+  }
+  __stcs(reinterpret_cast<uint2*>(static_cast<uint8_t*>(codes) + i), make_uint2(w[0], w[1]));
+  if (lane == 0) *sp = live ? __fdiv_rn(top, kE4m3Max) : 0.f;
+}
+
+template <int MAXT, typename PT, typename GT, bool MASTER, bool EIGHT>
+__global__ void __launch_bounds__(kAdamThreads)
+    salr_adamw_kernel(const __grid_constant__ AdamTable<MAXT> tab) {
+  __shared__ float sh[4];
+  const int lane = threadIdx.x & 31;
+  const int total = tab.start[tab.count];
+  const int warps = gridDim.x * (kAdamThreads / 32);
+  long long t = 0;
+  if (threadIdx.x == 0) {
+    t = tab.s.step[0] + 1;
+    const double lr = tab.s.lr_dev ? static_cast<double>(*tab.s.lr_dev) : tab.s.lr;
+    sh[0] = static_cast<float>(lr / (1.0 - adam_pow(tab.s.beta1, t)));
+    sh[1] = static_cast<float>(1.0 / sqrt(1.0 - adam_pow(tab.s.beta2, t)));
+    sh[2] = static_cast<float>(1.0 - lr * tab.s.weight_decay);
+    sh[3] = tab.s.grad_scale ? *tab.s.grad_scale : 1.f;
+  }
+  __syncthreads();
+  const float rate = sh[0], root = sh[1], decay = sh[2], gscale = sh[3];
+  const float eps = tab.s.eps, b1 = tab.s.b1, ob1 = tab.s.ob1, b2 = tab.s.b2, ob2 = tab.s.ob2;
+
+  for (int b = blockIdx.x * (kAdamThreads / 32) + (threadIdx.x >> 5); b < total; b += warps) {
+    int lo = 0, hi = tab.count;  // start[lo] <= b < start[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (tab.start[mid] <= b)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    const AdamTensor& e = tab.t[lo];
+    const int64_t blk = b - tab.start[lo];
+    const int64_t i = blk * kAdamBlock + lane * 8;
+    const int64_t left = e.n - i;
+    const int cnt = left >= 8 ? 8 : left > 0 ? static_cast<int>(left) : 0;
+    const bool vec = ((reinterpret_cast<uintptr_t>(e.param) | reinterpret_cast<uintptr_t>(e.grad)) & 15) == 0;
+    PT* const param = static_cast<PT*>(e.param);
+    float g[8], p[8], m[8], v[8];
+    uint2 mc, vc;
+    float ms = 0.f, vs = 0.f;
+    if (EIGHT) {
+      mc = adam_codes(e.m, i);
+      vc = adam_codes(e.v, i);
+      ms = e.m_scale[blk];
+      vs = e.v_scale[blk];
+    } else {
+      adam_get(static_cast<const float*>(e.m), i, cnt, true, m);
+      adam_get(static_cast<const float*>(e.v), i, cnt, true, v);
+    }
+    adam_get(static_cast<const GT*>(e.grad), i, cnt, vec, g);
+    if (MASTER)
+      adam_get(e.master, i, cnt, true, p);
+    else
+      adam_get(param, i, cnt, vec, p);
+    if (EIGHT) {
+      adam_decode(mc, ms, m);
+      adam_decode(vc, vs, v);
+    }
+    float r[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float gk = __fmul_rn(g[k], gscale);
+      if (EIGHT) v[k] = __fmul_rn(v[k], v[k]);
+      m[k] = __fadd_rn(__fmul_rn(m[k], b1), __fmul_rn(gk, ob1));
+      v[k] = __fadd_rn(__fmul_rn(v[k], b2), __fmul_rn(__fmul_rn(gk, gk), ob2));
+      r[k] = __fsqrt_rn(v[k]);
+      const float step = __fdiv_rn(m[k], __fadd_rn(__fmul_rn(r[k], root), eps));
+      p[k] = __fsub_rn(__fmul_rn(p[k], decay), __fmul_rn(rate, step));
+    }
+    if (EIGHT) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (k >= cnt) m[k] = r[k] = 0.f;  // past the tensor's end (codes there are padding)
+      adam_encode<false>(m, e.m, i, e.m_scale + blk, lane);
+      adam_encode<true>(r, e.v, i, e.v_scale + blk, lane);
+    } else {
+      adam_put(static_cast<float*>(e.m), i, cnt, true, m);
+      adam_put(static_cast<float*>(e.v), i, cnt, true, v);
+    }
+    if (MASTER) adam_put(e.master, i, cnt, true, p);
+    adam_put(param, i, cnt, vec, p);
+  }
+
+  // The last CTA of the step's last launch advances the step count: every CTA has read it
+  // by then (thread 0 reads it before it counts itself out).
+  if (tab.s.last) {
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      unsigned long long* done = reinterpret_cast<unsigned long long*>(tab.s.step + 1);
+      if (atomicAdd(done, 1ull) == gridDim.x - 1) {
+        *done = 0;
+        tab.s.step[0] = t;
+      }
+    }
+  }
+}
+
+}  // namespace salr

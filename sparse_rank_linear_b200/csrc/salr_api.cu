@@ -15,6 +15,7 @@
 
 #include "../../include/salr.h"
 #include "salr_codec.cuh"
+#include "salr_host.h"
 #include "salr_prefill.cuh"
 #include "salr_stream.cuh"
 #include "salr_svd.cuh"
@@ -106,19 +107,6 @@ bool valid_handle(salr_handle h) {
   return h && live().count(h) && h->magic == kMagic;
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-int cuda_status(cudaError_t e) {
-  if (e == cudaSuccess) return SALR_OK;
-  return e == cudaErrorMemoryAllocation ? SALR_ERR_OOM : SALR_ERR_CUDA;
-}
-
-#define SALR_TRY(expr)                      \
-  do {                                      \
-    const cudaError_t e_ = (expr);          \
-    if (e_ != cudaSuccess) return cuda_status(e_); \
-  } while (0)
-
 bool fake_oom() {
   const char* v = getenv("SALR_FAKE_OOM");
   return v && v[0] == '1';
@@ -185,15 +173,6 @@ cudaError_t alloc_handle_memory(salr_weight_s* h, int64_t blob_capacity, cudaStr
   h->offsets = reinterpret_cast<uint32_t*>(h->mem + 256);
   h->blob = h->mem + 256 + offs;
   return cudaSuccess;
-}
-
-int device_sms(int dev) {
-  static std::atomic<int> cache[64];  // zero-initialised: not looked up yet
-  if (dev >= 0 && dev < 64 && cache[dev]) return cache[dev];
-  int n = 0;
-  cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-  if (dev >= 0 && dev < 64) cache[dev] = n;
-  return n > 0 ? n : 1;
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
