@@ -334,6 +334,45 @@ SALR_API int salr_residual_adapter(const void* W, salr_handle h, int64_t r, cons
                                    void* stream);
 
 /*
+ * salr_q4_pack, salr_q4_encode - a weight held as 4-bit codes with group scales.
+ *
+ * The technical summary combines the method with 4-bit quantisation of the base weight
+ * (Experimental Results, QSALR) but defines no quantiser; this is the common uniform form:
+ *
+ *     W[n, k] = s[n, j] (q[n, k] - z[n, j]),   j = k / group,   q and z in 0 .. 15
+ *
+ * The handle they make stands wherever a weight is applied: salr_linear, salr_linear_host,
+ * salr_linear_backward, salr_decode, salr_info (nnz = N K; bytes = codes, scales and zero
+ * points), salr_sync_status and salr_free.  Calls that are about the bitmap form
+ * (salr_format_view, salr_save_size, salr_save, salr_residual_adapter) and
+ * salr_linear_noalloc return SALR_ERR_UNSUPPORTED for it.
+ *
+ * codes    device, 16-byte aligned, N x K / 2 bytes: q[n, 2i] in the low and q[n, 2i + 1]
+ *          in the high nibble of byte i of row n.
+ * scales   device, N x (K / group) bf16.
+ * zeros    device, N x (K / group) bytes, or NULL for 8 everywhere.  A value above 15
+ *          makes the call fail with SALR_ERR_INVALID.
+ * group    32, 64 or 128; K must be a multiple of it (else SALR_ERR_UNSUPPORTED).
+ * W        device, N x K bf16.  salr_q4_encode rounds each value to the nearest code, with
+ *          s = max|w| / 7 and z = 8 (symmetric != 0), or s = (max(w, 0) - min(w, 0)) / 15
+ *          and z = round(-min(w, 0) / s) (symmetric == 0), s rounded to bf16 first.  A value
+ *          of W that is not finite makes the call fail with SALR_ERR_INVALID.
+ * The arrays may be freed once the call returns; it synchronises `stream` once.
+ *
+ * salr_linear on such a handle: for M <= 64 the codes are rebuilt in registers (q - z
+ * exactly, in bf16), products and sums are fp32, each group's sum is scaled in fp32, t =
+ * X A_cat stays fp32, and results repeat bit for bit.  Two kernels with adapters, one
+ * without.  Above that, the weight is expanded to a dense bf16 scratch (s (q - z) rounded
+ * once) and the rest is as described under salr_linear.  The handle must be on the current
+ * device (else SALR_ERR_INVALID); its t buffer (M <= 64) is not safe to share between calls
+ * that run concurrently on different streams, captured graphs among them.
+ */
+SALR_API int salr_q4_pack(const void* codes, const void* scales, const void* zeros, int64_t N,
+                          int64_t K, int64_t group, void* stream, salr_handle* out);
+SALR_API int salr_q4_encode(const void* W, int64_t N, int64_t K, int64_t group, int symmetric,
+                            void* stream, salr_handle* out);
+
+/*
  * salr_adamw - one AdamW step over many tensors (the adapters of a model) at once.
  *
  * Defined by: the adapters, the residual adapter among them, are what fine-tuning trains

@@ -5,9 +5,10 @@ bitmap plus compact values; one hand-written CUDA kernel per call.  The Python l
 a ctypes binding of the C ABI in ``include/salr.h``; importing it does not load the
 library, the first call does (and fails loudly if it has not been built).
 """
-from .binding import (SIGNATURES, SalrError, SalrPlan, Weight, encode, linear, linear_host,
-                      load, load_library, plan, residual_adapter, status_string)
+from .binding import (SIGNATURES, SalrError, SalrPlan, Weight, encode, encode_q4, linear,
+                      linear_host, load, load_library, pack_q4, plan, residual_adapter,
+                      status_string)
 from .optim import AdamW
 
-__all__ = ["AdamW", "SIGNATURES", "SalrError", "SalrPlan", "Weight", "encode", "linear", "linear_host",
-           "load", "load_library", "plan", "residual_adapter", "status_string"]
+__all__ = ["AdamW", "SIGNATURES", "SalrError", "SalrPlan", "Weight", "encode", "encode_q4", "linear",
+           "linear_host", "load", "load_library", "pack_q4", "plan", "residual_adapter", "status_string"]

@@ -65,6 +65,8 @@ SIGNATURES = {
     "salr_load": (_I, [_P, _I64, _P, ctypes.POINTER(_P)]),
     "salr_residual_adapter": (_I, [_P, _P, _I64, _P, _I64, _I, _P, _P, _P, _P]),
     "salr_linear_plan": (_I, [_I64, _I64, _I64, _I64, ctypes.c_int32, ctypes.POINTER(SalrPlan)]),
+    "salr_q4_pack": (_I, [_P, _P, _P, _I64, _I64, _I64, _P, ctypes.POINTER(_P)]),
+    "salr_q4_encode": (_I, [_P, _I64, _I64, _I64, _I, _P, ctypes.POINTER(_P)]),
     "salr_adamw": (_I, [ctypes.POINTER(AdamwTensor), _I64, ctypes.POINTER(AdamwConfig), _P]),
     "salr_sync_status": (_I, [_P, _P]),
     "salr_status_string": (ctypes.c_char_p, [_I]),
@@ -128,10 +130,19 @@ def _require(t, name, shape=None, device=True):
 
 
 class Weight:
-    """An encoded (pruned, bitmap-stored) weight: owns a ``salr_handle``."""
+    """An encoded weight (pruned and bitmap-stored, or 4-bit codes with group scales): owns
+    a ``salr_handle``."""
 
     def __init__(self, handle: ctypes.c_void_p):
         self._h = handle
+        self._nk = None
+
+    def _shape(self):
+        """(N, K), which never change, looked up once."""
+        if self._nk is None:
+            inf = self.info()
+            self._nk = (inf["N"], inf["K"])
+        return self._nk
 
     @property
     def handle(self):
@@ -217,6 +228,47 @@ def encode(W, sparsity: float = 0.5, stream=None) -> Weight:
     return Weight(h)
 
 
+def pack_q4(codes, scales, zeros=None, stream=None) -> Weight:
+    """salr_q4_pack: a weight from 4-bit codes (N x K/2 uint8, even column in the low
+    nibble), bf16 scales and optional uint8 zero points (both N x K/group); CUDA tensors."""
+    import torch
+    for t, name, kind in ((codes, "codes", torch.uint8), (scales, "scales", torch.bfloat16),
+                          (zeros, "zeros", torch.uint8)):
+        if t is None and name == "zeros":
+            continue
+        if t.dtype != kind:
+            raise TypeError(f"{name} must be {str(kind)[6:]}")
+        if t.dim() != 2 or not t.is_contiguous() or not t.is_cuda:
+            raise ValueError(f"{name} must be a contiguous 2-D CUDA tensor")
+        if t.device != codes.device or t.shape[0] != codes.shape[0]:
+            raise ValueError(f"{name} must have codes' rows and device")
+    N, K = codes.shape[0], 2 * codes.shape[1]
+    if zeros is not None and zeros.shape != scales.shape:
+        raise ValueError("zeros must have the shape of scales")
+    if not scales.shape[1] or K % scales.shape[1]:
+        raise ValueError("scales must have one column per group of equal size")
+    h = _P()
+    with torch.cuda.device(codes.device):
+        _check("salr_q4_pack", load_library().salr_q4_pack(
+            _ptr(codes), _ptr(scales), _ptr(zeros), N, K, K // scales.shape[1],
+            _stream_ptr(stream), ctypes.byref(h)))
+    return Weight(h)
+
+
+def encode_q4(W, group: int = 64, symmetric: bool = True, stream=None) -> Weight:
+    """salr_q4_encode: round ``W`` (N x K bf16, CUDA) to 4-bit codes with a bf16 scale, and a
+    zero point unless ``symmetric``, per ``group`` columns of a row."""
+    import torch
+    _require(W, "W")
+    N, K = W.shape
+    h = _P()
+    with torch.cuda.device(W.device):
+        _check("salr_q4_encode", load_library().salr_q4_encode(
+            _ptr(W), N, K, int(group), 1 if symmetric else 0, _stream_ptr(stream),
+            ctypes.byref(h)))
+    return Weight(h)
+
+
 def load(image: bytes, stream=None) -> Weight:
     """salr_load: a weight on the current CUDA device from a serialised image."""
     data = bytes(image)
@@ -256,19 +308,20 @@ def residual_adapter(W, weight: Weight, r: int, q: int = 2, oversample: int = 16
 def linear(X, weight: Weight, A_cat=None, B_cat=None, Y=None, stream=None):
     """salr_linear: Y = X (M.W)^T + (X A_cat) B_cat; returns Y (M x N bf16)."""
     import torch
-    inf = weight.info()
+    N, K = weight._shape()
     _require(X, "X")
     M = X.shape[0]
-    if X.shape[1] != inf["K"]:
+    if X.shape[1] != K:
         raise ValueError("X has the wrong number of columns")
     R = 0
     if A_cat is not None:
         R = A_cat.shape[1]
-        _require(A_cat, "A_cat", (inf["K"], R))
-        _require(B_cat, "B_cat", (R, inf["N"]))
+        _require(A_cat, "A_cat", (K, R))
+        _require(B_cat, "B_cat", (R, N))
     if Y is None:
-        Y = torch.empty(M, inf["N"], dtype=torch.bfloat16, device=X.device)
-    _require(Y, "Y", (M, inf["N"]))
+        Y = torch.empty(M, N, dtype=torch.bfloat16, device=X.device)
+    else:
+        _require(Y, "Y", (M, N))
     _check("salr_linear", load_library().salr_linear(_ptr(X), M, weight.handle, _ptr(A_cat),
                                                      _ptr(B_cat), R, _ptr(Y), _stream_ptr(stream)))
     return Y

@@ -17,6 +17,7 @@
 #include "salr_codec.cuh"
 #include "salr_host.h"
 #include "salr_prefill.cuh"
+#include "salr_q4.cuh"
 #include "salr_stream.cuh"
 #include "salr_svd.cuh"
 
@@ -92,6 +93,9 @@ struct salr_weight_s {
   size_t x_cap;
   uint8_t* y_stage;
   size_t y_cap;
+  int group;     // 4-bit weights: columns per scale; 0: bitmap weight
+  Q4View q4;     // 4-bit weights: the packed codes, scales and zero points, in mem
+  float* q4_t;   // 4-bit weights: t = X A_cat of the small-M kernel, 64 x 128 fp32, in mem
 };
 
 namespace {
@@ -288,9 +292,24 @@ int ensure_tscratch(salr_weight_s* h, int64_t M, cudaStream_t st) {
   return SALR_OK;
 }
 
-// The dense expansion: as many CTAs as share the SMs (about 51 KB of shared memory each),
-// each walking several blocks so that staging the next one overlaps expanding this one.
+template <int GROUP>
+cudaError_t launch_q4_expand(const salr_weight_s* h, uint16_t* out, cudaStream_t st) {
+  const long long units = h->N / 16 * h->q4.units;
+  const unsigned g = static_cast<unsigned>(std::min<long long>((units + 7) / 8, 8ll * device_sms(h->device)));
+  if (h->q4.zeros)
+    q4_expand_kernel<GROUP, true><<<g, 256, 0, st>>>(h->q4, out);
+  else
+    q4_expand_kernel<GROUP, false><<<g, 256, 0, st>>>(h->q4, out);
+  return cudaGetLastError();
+}
+
+// The dense expansion.  Bitmap weights: as many CTAs as share the SMs (about 51 KB of
+// shared memory each), each walking several blocks so that staging the next one overlaps
+// expanding this one.
 cudaError_t launch_expand(const salr_weight_s* h, uint16_t* out, cudaStream_t st) {
+  if (h->group == 32) return launch_q4_expand<32>(h, out, st);
+  if (h->group == 64) return launch_q4_expand<64>(h, out, st);
+  if (h->group == 128) return launch_q4_expand<128>(h, out, st);
   static std::atomic<bool> attr_set[64];  // zero-initialised: false
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -403,7 +422,8 @@ struct LinearPlan {
   int64_t sum_bytes, dense_bytes;
   int group_rows;  // prefill tile order (tile_group_rows)
 };
-LinearPlan plan_linear(int64_t N, int64_t K, int64_t M, int64_t R, int sms) {
+// `dense_only`: the weight has no fused decoder (4-bit weights): path 2 for every M > 64.
+LinearPlan plan_linear(int64_t N, int64_t K, int64_t M, int64_t R, int sms, bool dense_only) {
   LinearPlan p{};
   p.RT = static_cast<int>(N / 128);
   p.KB = static_cast<int>(K / 64);
@@ -417,7 +437,7 @@ LinearPlan plan_linear(int64_t N, int64_t K, int64_t M, int64_t R, int sms) {
   }
   p.bnt = M <= 128 ? 128 : 256;
   p.TT = static_cast<int>((M + p.bnt - 1) / p.bnt);
-  const bool dense = p.TT >= kDenseMinTokenTiles;
+  const bool dense = dense_only || p.TT >= kDenseMinTokenTiles;
   // Dense weight tiles of 256 rows let two MMAs share every X tile: a third fewer operand
   // bytes through shared memory per MMA cycle.  Their two accumulators fill the TMEM, so
   // a unit's epilogue no longer overlaps the next unit's MMAs; that costs a few us per
@@ -668,6 +688,12 @@ int launch_stream(StreamParams p, const CUtensorMap& tx, const CUtensorMap& ta,
 // GPU's memory anyway.
 bool too_many_tiles(int64_t N, int64_t M) { return (N / 128) * ((M + 127) / 128) > (1ll << 27); }
 
+// Whether the handle lives on the current device.
+bool on_current_device(salr_handle h) {
+  int dev = -1;
+  return cudaGetDevice(&dev) == cudaSuccess && dev == h->device;
+}
+
 int check_linear_args(const void* X, int64_t M, salr_handle h, const void* A, const void* B,
                       int64_t R, const void* Y) {
   if (!valid_handle(h)) return SALR_ERR_INVALID;
@@ -680,6 +706,54 @@ int check_linear_args(const void* X, int64_t M, salr_handle h, const void* A, co
   if (!aligned16(X) || !aligned16(Y) || (R > 0 && (!aligned16(A) || !aligned16(B))))
     return SALR_ERR_UNSUPPORTED;
   return SALR_OK;
+}
+
+template <int NT, int GROUP>
+int launch_q4(const salr_weight_s* h, const uint16_t* X, int M, const float* t, const uint16_t* B,
+              int R, uint16_t* Y, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(h->N / 16));
+  cfg.blockDim = dim3(32 * kQ4Warps);
+  cfg.stream = st;
+  // Directly after the t kernel, the launch may overlap it: codes, X and B were complete
+  // before that kernel started, and t is waited for.
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = R > 0 ? 1 : 0;
+  if (h->q4.zeros)
+    SALR_TRY(cudaLaunchKernelEx(&cfg, q4_linear_kernel<NT, GROUP, true>, h->q4, X, M, t, B, R, Y));
+  else
+    SALR_TRY(cudaLaunchKernelEx(&cfg, q4_linear_kernel<NT, GROUP, false>, h->q4, X, M, t, B, R, Y));
+  return SALR_OK;
+}
+
+// The layer on a 4-bit weight for up to 64 tokens: a t kernel (with adapters) and the
+// layer kernel, which starts while t is being computed.
+int launch_q4_linear(const void* Xv, int64_t M64, salr_handle h, const void* A, const void* Bv,
+                     int64_t R64, void* Yv, cudaStream_t st) {
+  const int M = static_cast<int>(M64), R = static_cast<int>(R64), K = static_cast<int>(h->K);
+  const uint16_t* X = static_cast<const uint16_t*>(Xv);
+  const uint16_t* B = static_cast<const uint16_t*>(Bv);
+  uint16_t* Y = static_cast<uint16_t*>(Yv);
+  if (R > 0) {
+    const uint16_t* Ab = static_cast<const uint16_t*>(A);
+    if (M == 1)
+      q4_t_kernel<1><<<dim3(R / 8, 1), kQ4TThreads, 0, st>>>(X, Ab, M, K, R, h->q4_t);
+    else
+      q4_t_kernel<8><<<dim3(R / 8, (M + 7) / 8), kQ4TThreads, 0, st>>>(X, Ab, M, K, R, h->q4_t);
+    SALR_TRY(cudaGetLastError());
+  }
+#define SALR_Q4_TOKENS(NT)                                                     \
+  return h->group == 32   ? launch_q4<NT, 32>(h, X, M, h->q4_t, B, R, Y, st)   \
+         : h->group == 64 ? launch_q4<NT, 64>(h, X, M, h->q4_t, B, R, Y, st)   \
+                          : launch_q4<NT, 128>(h, X, M, h->q4_t, B, R, Y, st)
+  if (M <= 8) SALR_Q4_TOKENS(1);
+  if (M <= 16) SALR_Q4_TOKENS(2);
+  if (M <= 32) SALR_Q4_TOKENS(4);
+  SALR_Q4_TOKENS(8);
+#undef SALR_Q4_TOKENS
 }
 
 }  // namespace
@@ -841,6 +915,129 @@ int salr_encode(const void* W, int64_t N, int64_t K, float sparsity, void* strea
   return SALR_OK;
 }
 
+}  // extern "C"
+
+namespace {
+
+bool valid_group(int64_t K, int64_t group) {
+  return (group == 32 || group == 64 || group == 128) && K % group == 0;
+}
+
+// Checks shared by salr_q4_pack and salr_q4_encode.
+int check_q4_shape(int64_t N, int64_t K, int64_t group) {
+  const int shape = check_shape(N, K);
+  if (shape != SALR_OK) return shape;
+  return valid_group(K, group) ? SALR_OK : SALR_ERR_UNSUPPORTED;
+}
+
+// A new handle from row-major codes, scales and zero points on the device, checked: waits
+// for `st`, which also may hold the work that makes those arrays and sets `status` bits.
+// `scratch`: pool memory released on `st` either way.
+int q4_make(const void* codes, const void* scales, const void* zeros, int64_t N, int64_t K,
+            int64_t group, int* flags, void* scratch, cudaStream_t st, salr_handle* out) {
+  salr_weight_s* h = new (std::nothrow) salr_weight_s();
+  if (!h) {
+    if (scratch) cudaFreeAsync(scratch, st);
+    return SALR_ERR_OOM;
+  }
+  std::memset(h, 0, sizeof(*h));
+  cudaGetDevice(&h->device);
+  h->N = N;
+  h->K = K;
+  h->keep = K;
+  h->nnz = N * K;
+  h->group = static_cast<int>(group);
+  const int units = static_cast<int>((K + kQ4Unit - 1) / kQ4Unit);
+  const int64_t all = N / 16 * units;
+  const int64_t pairs = all * 8 * (kQ4Unit / group);
+  const size_t cb = round256(all * kQ4UnitBytes), sb = round256(pairs * 4);
+  const size_t zb = zeros ? round256(pairs * 2) : 0;
+  auto fail = [&](int code) {
+    if (scratch) cudaFreeAsync(scratch, st);
+    cudaStreamSynchronize(st);
+    release(h);
+    return code;
+  };
+  cudaError_t e;
+  const size_t tb = kQ4MaxTokens * 128 * sizeof(float);
+  if ((e = alloc_handle_memory(h, cb + sb + zb + tb, st)) != cudaSuccess) return fail(cuda_status(e));
+  h->q4.codes = h->blob;
+  h->q4.scales = reinterpret_cast<const uint32_t*>(h->blob + cb);
+  h->q4.zeros = zeros ? reinterpret_cast<const uint16_t*>(h->blob + cb + sb) : nullptr;
+  h->q4_t = reinterpret_cast<float*>(h->blob + cb + sb + zb);
+  h->q4.N = static_cast<int>(N);
+  h->q4.K = static_cast<int>(K);
+  h->q4.units = units;
+  h->blob_bytes = all * kQ4UnitBytes + pairs * (zeros ? 6 : 4);
+  if ((e = cudaMemsetAsync(h->status, 0, sizeof(int), st)) != cudaSuccess) return fail(cuda_status(e));
+  const long long words = all * (kQ4UnitBytes / 4);
+  const unsigned grid = static_cast<unsigned>(std::min<long long>((words + 255) / 256, 16ll * device_sms(h->device)));
+  q4_pack_kernel<<<grid, 256, 0, st>>>(
+      static_cast<const uint32_t*>(codes), static_cast<const uint16_t*>(scales),
+      static_cast<const uint8_t*>(zeros), h->q4.N, h->q4.K, h->group, units,
+      reinterpret_cast<uint32_t*>(h->blob), reinterpret_cast<uint32_t*>(h->blob + cb),
+      reinterpret_cast<uint16_t*>(h->blob + cb + sb), h->status);
+  if ((e = cudaGetLastError()) != cudaSuccess) return fail(cuda_status(e));
+  int status[2] = {0, 0};
+  if ((e = cudaMemcpyAsync(status, h->status, sizeof(int), cudaMemcpyDeviceToHost, st)) != cudaSuccess ||
+      (flags && (e = cudaMemcpyAsync(status + 1, flags, sizeof(int), cudaMemcpyDeviceToHost, st)) != cudaSuccess))
+    return fail(cuda_status(e));
+  if (scratch) {
+    e = cudaFreeAsync(scratch, st);
+    scratch = nullptr;
+    if (e != cudaSuccess) return fail(cuda_status(e));
+  }
+  if ((e = cudaStreamSynchronize(st)) != cudaSuccess) return fail(cuda_status(e));
+  if (status[0] | status[1]) return fail(SALR_ERR_INVALID);
+  publish(h, out);
+  return SALR_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int salr_q4_pack(const void* codes, const void* scales, const void* zeros, int64_t N, int64_t K,
+                 int64_t group, void* stream, salr_handle* out) {
+  if (!codes || !scales || !out) return SALR_ERR_INVALID;
+  const int shape = check_q4_shape(N, K, group);
+  if (shape != SALR_OK) return shape;
+  if (!aligned16(codes) || (reinterpret_cast<uintptr_t>(scales) & 1u)) return SALR_ERR_UNSUPPORTED;
+  return q4_make(codes, scales, zeros, N, K, group, nullptr, nullptr, static_cast<cudaStream_t>(stream), out);
+}
+
+int salr_q4_encode(const void* W, int64_t N, int64_t K, int64_t group, int symmetric, void* stream,
+                   salr_handle* out) {
+  if (!W || !out) return SALR_ERR_INVALID;
+  const int shape = check_q4_shape(N, K, group);
+  if (shape != SALR_OK) return shape;
+  if (!aligned16(W)) return SALR_ERR_UNSUPPORTED;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  int dev = 0;
+  SALR_TRY(cudaGetDevice(&dev));
+  // scratch: [flags][codes][scales][zero points]
+  const size_t cb = round256(static_cast<size_t>(N) * K / 2), ng = static_cast<size_t>(N) * (K / group);
+  const size_t sb = round256(ng * 2), zb = symmetric ? 0 : round256(ng);
+  uint8_t* mem = nullptr;
+  SALR_TRY(dev_alloc_async(reinterpret_cast<void**>(&mem), 256 + cb + sb + zb, st));
+  uint8_t *codes = mem + 256, *scales = codes + cb, *zeros = symmetric ? nullptr : scales + sb;
+  int* flags = reinterpret_cast<int*>(mem);
+  cudaError_t e = cudaMemsetAsync(flags, 0, sizeof(int), st);
+  if (e == cudaSuccess) {
+    const long long warps = static_cast<long long>(N) * ((K + kQ4Unit - 1) / kQ4Unit);
+    const unsigned grid = static_cast<unsigned>(std::min<long long>((warps + 7) / 8, 8ll * device_sms(dev)));
+    q4_quantise_kernel<<<grid, 256, 0, st>>>(
+        static_cast<const uint16_t*>(W), static_cast<int>(N), static_cast<int>(K), static_cast<int>(group),
+        symmetric ? 1 : 0, reinterpret_cast<uint32_t*>(codes), reinterpret_cast<uint16_t*>(scales), zeros, flags);
+    e = cudaGetLastError();
+  }
+  if (e != cudaSuccess) {
+    cudaFreeAsync(mem, st);
+    return cuda_status(e);
+  }
+  return q4_make(codes, scales, zeros, N, K, group, flags, mem, st, out);
+}
+
 int salr_decode(salr_handle h, void* W_out, void* stream) {
   if (!valid_handle(h) || !W_out) return SALR_ERR_INVALID;
   if (!aligned16(W_out)) return SALR_ERR_UNSUPPORTED;
@@ -862,7 +1059,7 @@ int salr_linear_plan(int64_t N, int64_t K, int64_t M, int64_t R, int32_t sms, sa
     }
     sms = n;
   }
-  const LinearPlan p = plan_linear(N, K, M, R, sms);
+  const LinearPlan p = plan_linear(N, K, M, R, sms, false);
   out->path = p.path;
   out->kernels = p.kernels;
   out->token_tile = p.bnt;
@@ -883,6 +1080,8 @@ int salr_linear(const void* X, int64_t M, salr_handle h, const void* A_cat, cons
   int rc = check_linear_args(X, M, h, A_cat, B_cat, R, Y);
   if (rc != SALR_OK) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (h->group && !on_current_device(h)) return SALR_ERR_INVALID;
+  if (h->group && M <= kQ4MaxTokens) return launch_q4_linear(X, M, h, A_cat, B_cat, R, Y, st);
   if (M <= 64) {
     rc = ensure_stream_scratch(h, st);
     if (rc != SALR_OK) return rc;
@@ -923,7 +1122,7 @@ int salr_linear(const void* X, int64_t M, salr_handle h, const void* A_cat, cons
   // prefill shapes: t = X A_cat once (own kernel), then the fused decode + GEMM
   const int sms = device_sms(h->device);
   if (h->K / 64 > kPreMaxKBlocks) return SALR_ERR_UNSUPPORTED;
-  const LinearPlan pl = plan_linear(h->N, h->K, M, R, sms);
+  const LinearPlan pl = plan_linear(h->N, h->K, M, R, sms, h->group != 0);
   const int bnt = pl.bnt, TT = pl.TT, KB = pl.KB;
   const int R16 = static_cast<int>((R + 15) / 16 * 16);
   CUtensorMap tx, ta, tb, tt;
@@ -1059,13 +1258,15 @@ int salr_info(salr_handle h, int64_t* N, int64_t* K, int64_t* nnz, int64_t* byte
   if (N) *N = h->N;
   if (K) *K = h->K;
   if (nnz) *nnz = h->nnz;
-  if (bytes) *bytes = h->blob_bytes + (h->nblocks + 1) * static_cast<int64_t>(sizeof(uint32_t));
+  if (bytes)
+    *bytes = h->blob_bytes + (h->group ? 0 : (h->nblocks + 1) * static_cast<int64_t>(sizeof(uint32_t)));
   return SALR_OK;
 }
 
 int salr_format_view(salr_handle h, const void** blob, int64_t* blob_bytes, const void** offsets,
                      int64_t* n_offsets) {
   if (!valid_handle(h)) return SALR_ERR_INVALID;
+  if (h->group) return SALR_ERR_UNSUPPORTED;
   if (blob) *blob = h->blob;
   if (blob_bytes) *blob_bytes = h->blob_bytes;
   if (offsets) *offsets = h->offsets;
@@ -1083,13 +1284,16 @@ int salr_format_view(salr_handle h, const void** blob, int64_t* blob_bytes, cons
 // ------------------------------------------------------------------------------------
 int salr_save_size(salr_handle h, int64_t* bytes) {
   if (!valid_handle(h) || !bytes) return SALR_ERR_INVALID;
+  if (h->group) return SALR_ERR_UNSUPPORTED;
   *bytes = kImageHeader + image_offsets_bytes(h->nblocks) + h->blob_bytes;
   return SALR_OK;
 }
 
 int salr_save(salr_handle h, void* buf, int64_t buf_bytes, void* stream) {
   int64_t need = 0;
-  if (salr_save_size(h, &need) != SALR_OK || !buf) return SALR_ERR_INVALID;
+  const int sized = salr_save_size(h, &need);
+  if (sized != SALR_OK) return sized;
+  if (!buf) return SALR_ERR_INVALID;
   if (buf_bytes < need) return SALR_ERR_INVALID;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   uint8_t* out = static_cast<uint8_t*>(buf);
@@ -1279,6 +1483,7 @@ extern "C" {
 int salr_residual_adapter(const void* W, salr_handle h, int64_t r, const void* omega, int64_t l,
                           int q, void* A_out, void* B_out, void* sigma_out, void* stream) {
   if (!valid_handle(h) || !W || !omega || !A_out || !B_out) return SALR_ERR_INVALID;
+  if (h->group) return SALR_ERR_UNSUPPORTED;
   if (r < 1 || l < r || l > kSvdMaxL || l > h->N || l > h->K || q < 0 || q > 16)
     return SALR_ERR_INVALID;
   if (!aligned16(W) || (reinterpret_cast<uintptr_t>(omega) & 3u) ||
@@ -1505,7 +1710,7 @@ extern "C" int salr_linear_noalloc(const void* X, int64_t M, salr_handle h, cons
                                    const void* B_cat, int64_t R, void* Y, void* stream) {
   int rc = check_linear_args(X, M, h, A_cat, B_cat, R, Y);
   if (rc != SALR_OK) return rc;
-  if (M > kNoAllocMaxM || h->N > kNoAllocMaxN) return SALR_ERR_UNSUPPORTED;
+  if (h->group || M > kNoAllocMaxM || h->N > kNoAllocMaxN) return SALR_ERR_UNSUPPORTED;
   int dev = 0;
   SALR_TRY(cudaGetDevice(&dev));
   if (dev != h->device) return SALR_ERR_INVALID;
