@@ -24,8 +24,9 @@
  *   - Every call returns a salr_status.  Argument errors are detected on the host before
  *     any work is queued; nothing is written in that case.
  *   - Handles and the scratch of salr_encode, salr_load and salr_residual_adapter take
- *     device memory from a stream-ordered pool the library owns on each device; memory
- *     given back to it stays reserved for reuse, up to 1 GiB per device.
+ *     device memory from a stream-ordered pool the library owns on each device, and the
+ *     transient scratch of salr_linear and salr_linear_backward from a second one; memory
+ *     given back to a pool stays reserved for reuse, up to 1 GiB per pool and device.
  *   - The library never traps or spins without a bound on the GPU.  Errors found on the
  *     device (a NaN in W, a pipeline wait that ran out of time) are recorded in the
  *     handle's status word; salr_encode reports them itself, salr_sync_status reads them.
@@ -371,6 +372,41 @@ SALR_API int salr_q4_pack(const void* codes, const void* scales, const void* zer
                           int64_t K, int64_t group, void* stream, salr_handle* out);
 SALR_API int salr_q4_encode(const void* W, int64_t N, int64_t K, int64_t group, int symmetric,
                             void* stream, salr_handle* out);
+
+/*
+ * salr_linear_backward - the gradients of salr_linear for a frozen weight W_h (the one the
+ * handle stands for, bitmap or 4-bit):
+ *
+ *     dX = dY W_h + (dY B_cat^T) A_cat^T      dA = X^T (dY B_cat^T)      dB = (X A_cat)^T dY
+ *
+ * Defined by: the adapters (residual and task LoRAs) are what fine-tuning trains, the base
+ * weight is frozen (technical summary, Methodology 1 to 3); the formulas are the chain rule.
+ *
+ * dY    device, M x N bf16: the gradient of the loss with respect to Y.
+ * X     device, M x K bf16: the layer's input.  Needed for dA or dB only (else may be NULL).
+ * A_cat, B_cat, R  as for salr_linear.
+ * dX    device, M x K bf16; dA device, K x R bf16; dB device, R x N bf16: overwritten.  Any
+ *       of them may be NULL (not wanted), but not all; dA and dB need R > 0.  None may
+ *       overlap an input or another output.
+ *
+ * Arithmetic: products of bf16 values accumulate in fp32 on the tensor cores; dY B_cat^T and
+ * X A_cat are kept as two bf16 parts (16 bits of significand); a 4-bit weight enters as the
+ * bf16 rounding that salr_decode gives.  Each output is rounded once, and results repeat
+ * bit for bit.
+ *
+ * Two to four kernels and a memset, with scratch from the library's pool taken on `stream`
+ * and given back to it in stream order: with dX the dense weight (2 N K bytes), and 8 to 16
+ * bytes per token and rank.  Nothing of the handle is written but its status word, so calls
+ * on one handle may run concurrently on several streams; captured, a call keeps its scratch
+ * as the graph's own.
+ *
+ * SALR_ERR_INVALID: a bad handle or one of another device, a NULL dY, all outputs NULL, dA
+ * or dB with R == 0 or a NULL X, R > 0 with a NULL adapter, M < 1, R < 0.
+ * SALR_ERR_UNSUPPORTED: M, R or alignment outside the shape rules.
+ */
+SALR_API int salr_linear_backward(const void* dY, const void* X, int64_t M, salr_handle h,
+                                  const void* A_cat, const void* B_cat, int64_t R, void* dX,
+                                  void* dA, void* dB, void* stream);
 
 /*
  * salr_adamw - one AdamW step over many tensors (the adapters of a model) at once.

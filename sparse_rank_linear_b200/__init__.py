@@ -6,9 +6,9 @@ a ctypes binding of the C ABI in ``include/salr.h``; importing it does not load 
 library, the first call does (and fails loudly if it has not been built).
 """
 from .binding import (SIGNATURES, SalrError, SalrPlan, Weight, encode, encode_q4, linear,
-                      linear_host, load, load_library, pack_q4, plan, residual_adapter,
+                      linear_backward, linear_host, load, load_library, pack_q4, plan, residual_adapter,
                       status_string)
 from .optim import AdamW
 
 __all__ = ["AdamW", "SIGNATURES", "SalrError", "SalrPlan", "Weight", "encode", "encode_q4", "linear",
-           "linear_host", "load", "load_library", "pack_q4", "plan", "residual_adapter", "status_string"]
+           "linear_backward", "linear_host", "load", "load_library", "pack_q4", "plan", "residual_adapter", "status_string"]

@@ -67,6 +67,7 @@ SIGNATURES = {
     "salr_linear_plan": (_I, [_I64, _I64, _I64, _I64, ctypes.c_int32, ctypes.POINTER(SalrPlan)]),
     "salr_q4_pack": (_I, [_P, _P, _P, _I64, _I64, _I64, _P, ctypes.POINTER(_P)]),
     "salr_q4_encode": (_I, [_P, _I64, _I64, _I64, _I, _P, ctypes.POINTER(_P)]),
+    "salr_linear_backward": (_I, [_P, _P, _I64, _P, _P, _P, _I64, _P, _P, _P, _P]),
     "salr_adamw": (_I, [ctypes.POINTER(AdamwTensor), _I64, ctypes.POINTER(AdamwConfig), _P]),
     "salr_sync_status": (_I, [_P, _P]),
     "salr_status_string": (ctypes.c_char_p, [_I]),
@@ -325,6 +326,47 @@ def linear(X, weight: Weight, A_cat=None, B_cat=None, Y=None, stream=None):
     _check("salr_linear", load_library().salr_linear(_ptr(X), M, weight.handle, _ptr(A_cat),
                                                      _ptr(B_cat), R, _ptr(Y), _stream_ptr(stream)))
     return Y
+
+
+def linear_backward(dY, X, weight: Weight, A_cat=None, B_cat=None, dX=None, dA=None, dB=None,
+                    needs=(True, True, True), stream=None):
+    """salr_linear_backward: the gradients (dX, dA, dB) of ``linear`` for the gradient ``dY``
+    of its result (M x N bf16).  ``needs`` says which are wanted; the others, and dA and dB
+    without adapters, come back as None.  ``X`` may be None if only dX is wanted."""
+    import torch
+    N, K = weight._shape()
+    _require(dY, "dY")
+    if dY.dim() != 2 or dY.shape[1] != N:
+        raise ValueError("dY has the wrong number of columns")
+    M = dY.shape[0]
+    R = 0
+    if A_cat is not None:
+        R = A_cat.shape[1]
+        _require(A_cat, "A_cat", (K, R))
+        _require(B_cat, "B_cat", (R, N))
+    want_x, want_a, want_b = bool(needs[0]), bool(needs[1]) and R > 0, bool(needs[2]) and R > 0
+    if not (want_x or want_a or want_b):
+        raise ValueError("no gradient is wanted")
+    if want_a or want_b:
+        if X is None:
+            raise ValueError("X is needed for dA and dB")
+        _require(X, "X", (M, K))
+    out = []
+    for want, t, name, shape in ((want_x, dX, "dX", (M, K)), (want_a, dA, "dA", (K, R)),
+                                 (want_b, dB, "dB", (R, N))):
+        if not want:
+            t = None
+        elif t is None:
+            t = torch.empty(shape, dtype=torch.bfloat16, device=dY.device)
+        else:
+            _require(t, name, shape)
+        out.append(t)
+    dX, dA, dB = out
+    with torch.cuda.device(dY.device):
+        _check("salr_linear_backward", load_library().salr_linear_backward(
+            _ptr(dY), _ptr(X), M, weight.handle, _ptr(A_cat), _ptr(B_cat), R, _ptr(dX), _ptr(dA),
+            _ptr(dB), _stream_ptr(stream)))
+    return dX, dA, dB
 
 
 def linear_host(X_host, weight: Weight, A_cat, B_cat, Y_host, stream=None):

@@ -17,7 +17,7 @@ LIB = os.path.join(HERE, "libsalr.so")
 SOURCES = ["salr_api.cu", "salr_adamw.cu"]
 HEADERS = ["sm100.cuh", "salr_block.cuh", "salr_decode.cuh", "salr_codec.cuh", "salr_prefill.cuh",
            "salr_stream.cuh", "salr_svd.cuh", "salr_host.h", "salr_adamw.cuh",
-           "salr_q4.cuh"]
+           "salr_q4.cuh", "salr_grad.cuh"]
 
 
 def nvcc_path() -> str:

@@ -15,6 +15,7 @@
 
 #include "../../include/salr.h"
 #include "salr_codec.cuh"
+#include "salr_grad.cuh"
 #include "salr_host.h"
 #include "salr_prefill.cuh"
 #include "salr_q4.cuh"
@@ -121,14 +122,19 @@ cudaError_t dev_alloc(void** p, size_t bytes) {
   return cudaMalloc(p, bytes);
 }
 
-// The library's stream-ordered memory pool on each device.  Freed blocks stay reserved
-// for reuse up to 1 GiB (the default pool would hand them back to the driver at every
-// synchronisation, and mapping them again costs about as much as a cudaMalloc).
+// The library's stream-ordered memory pools on each device: one for handles and what makes
+// them, one for the scratch of a call.  Freed blocks stay reserved for reuse up to 1 GiB a
+// pool (the default pool would hand them back to the driver at every synchronisation, and
+// mapping them again costs about as much as a cudaMalloc).  The limit counts a pool's
+// memory in use too: scratch beside the handles of a whole model would be unmapped and
+// mapped again around every synchronisation.
 constexpr uint64_t kPoolKeepBytes = 1ull << 30;
+enum PoolKind { kPoolHandles = 0, kPoolScratch = 1 };
 
-cudaError_t library_pool(int dev, cudaMemPool_t* out) {
+cudaError_t library_pool(int dev, PoolKind kind, cudaMemPool_t* out) {
   static std::mutex mu;
-  static cudaMemPool_t pools[64] = {};
+  static cudaMemPool_t all_pools[2][64] = {};
+  cudaMemPool_t* const pools = all_pools[kind];
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   std::lock_guard<std::mutex> g(mu);
   if (!pools[dev]) {
@@ -152,14 +158,14 @@ cudaError_t library_pool(int dev, cudaMemPool_t* out) {
   return cudaSuccess;
 }
 
-// Stream-ordered allocation from the library pool (freed with cudaFreeAsync).
-cudaError_t dev_alloc_async(void** p, size_t bytes, cudaStream_t st) {
+// Stream-ordered allocation from a library pool (freed with cudaFreeAsync).
+cudaError_t dev_alloc_async(void** p, size_t bytes, cudaStream_t st, PoolKind kind = kPoolHandles) {
   if (fake_oom()) return cudaErrorMemoryAllocation;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   cudaMemPool_t pool;
-  if ((e = library_pool(dev, &pool)) != cudaSuccess) return e;
+  if ((e = library_pool(dev, kind, &pool)) != cudaSuccess) return e;
   return cudaMallocFromPoolAsync(p, bytes, pool, st);
 }
 
@@ -1169,7 +1175,8 @@ int salr_linear(const void* X, int64_t M, salr_handle h, const void* A_cat, cons
   pp.group_rows = pl.group_rows;
   if (pp.dense) {
     const cudaError_t e =
-        dev_alloc_async(reinterpret_cast<void**>(&wdense), static_cast<size_t>(h->N) * h->K * 2, st);
+        dev_alloc_async(reinterpret_cast<void**>(&wdense), static_cast<size_t>(h->N) * h->K * 2, st,
+                        kPoolScratch);
     if (e != cudaSuccess) return cuda_status(e);
     const cudaError_t le = launch_expand(h, reinterpret_cast<uint16_t*>(wdense), st);
     if (le != cudaSuccess || !make_map(&tw, wdense, h->K, h->N, 64, 128)) {
@@ -1410,6 +1417,206 @@ int salr_load(const void* buf, int64_t buf_bytes, void* stream, salr_handle* out
   cudaFree(nnz_d);
   publish(h, out);
   return SALR_OK;
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------------------------------
+// salr_linear_backward (salr_grad.cuh)
+// ------------------------------------------------------------------------------------
+namespace {
+
+// Parts of each tile's reduction, so that `slots` CTAs share `total` chunks evenly; a part
+// keeps at least 8 chunks (its fp32 sum costs a write and a read in L2).
+int grad_parts(int chunks, int64_t total, int slots) {
+  const int64_t each = std::max<int64_t>(8, (total + slots - 1) / slots);
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(chunks, (chunks + each - 1) / each)));
+}
+
+template <int BN>
+int launch_grad_skinny(const GradSkinnyParams& p, const CUtensorMap* m, cudaStream_t st) {
+  static std::atomic<bool> attr_set[64];  // zero-initialised: false
+  int dev = 0;
+  SALR_TRY(cudaGetDevice(&dev));
+  if (dev < 0 || dev >= 64) return SALR_ERR_UNSUPPORTED;
+  if (!attr_set[dev]) {
+    SALR_TRY(cudaFuncSetAttribute(grad_skinny_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  GradSkinny<BN>::kSmemBytes));
+    attr_set[dev] = true;
+  }
+  const unsigned grid = static_cast<unsigned>(p.units0 + p.p[1].tiles * p.p[1].parts);
+  grad_skinny_kernel<BN><<<grid, kGradThreads, GradSkinny<BN>::kSmemBytes, st>>>(p, m[0], m[1], m[2], m[3]);
+  SALR_TRY(cudaGetLastError());
+  return SALR_OK;
+}
+
+int launch_grad_dx(const GradDxParams& p, const CUtensorMap* m, int pairs, cudaStream_t st) {
+  static std::atomic<bool> attr_set[64];  // zero-initialised: false
+  int dev = 0;
+  SALR_TRY(cudaGetDevice(&dev));
+  if (dev < 0 || dev >= 64) return SALR_ERR_UNSUPPORTED;
+  if (!attr_set[dev]) {
+    SALR_TRY(cudaFuncSetAttribute(grad_dx_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kDxSmemBytes));
+    attr_set[dev] = true;
+  }
+  grad_dx_kernel<<<2 * pairs, kGradThreads, kDxSmemBytes, st>>>(p, m[0], m[1], m[2], m[3]);
+  SALR_TRY(cudaGetLastError());
+  return SALR_OK;
+}
+
+size_t grad_part_bytes(const GradProblem& p, int columns) {
+  return p.parts > 1 ? static_cast<size_t>(p.tiles) * p.parts * columns * 128 * sizeof(float) : 0;
+}
+
+}  // namespace
+
+extern "C" {
+
+int salr_linear_backward(const void* dY, const void* X, int64_t M64, salr_handle h, const void* A_cat,
+                         const void* B_cat, int64_t R64, void* dX, void* dA, void* dB, void* stream) {
+  if (!valid_handle(h) || !dY || M64 < 1 || R64 < 0) return SALR_ERR_INVALID;
+  if (!dX && !dA && !dB) return SALR_ERR_INVALID;
+  if (R64 == 0 && (dA || dB)) return SALR_ERR_INVALID;
+  if (R64 > 0 && (!A_cat || !B_cat)) return SALR_ERR_INVALID;
+  if ((dA || dB) && !X) return SALR_ERR_INVALID;
+  if (R64 % 8 != 0 || R64 > 128 || M64 > (1ll << 24) || too_many_tiles(h->N, M64) || too_many_tiles(h->K, M64))
+    return SALR_ERR_UNSUPPORTED;
+  if (!aligned16(dY) || !aligned16(X) || !aligned16(dX) || !aligned16(dA) || !aligned16(dB) ||
+      (R64 > 0 && (!aligned16(A_cat) || !aligned16(B_cat))))
+    return SALR_ERR_UNSUPPORTED;
+  if (!on_current_device(h)) return SALR_ERR_INVALID;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int M = static_cast<int>(M64), N = static_cast<int>(h->N), K = static_cast<int>(h->K);
+  const int R = static_cast<int>(R64), half = R <= 64 ? 64 : 128;
+  const int sms = device_sms(h->device), pairs = std::max(1, sms / 2);
+  const int mtiles = (M + 127) / 128, mchunks = (M + 63) / 64;
+  const bool want_u = R > 0 && (dX || dA), want_t = dB != nullptr;
+
+  // t and u
+  GradSkinnyParams s1{}, s2{};
+  s1.status = s2.status = h->status;
+  const int slots1 = 2 * sms;
+  const int64_t total1 = static_cast<int64_t>(mtiles) * ((want_t ? K / 64 : 0) + (want_u ? N / 64 : 0));
+  GradProblem &pt = s1.p[0], &pu = s1.p[1];
+  pt.tiles = want_t ? mtiles : 0;
+  pt.chunks = K / 64;
+  pt.b_mn = 1;
+  pu.tiles = want_u ? mtiles : 0;
+  pu.chunks = N / 64;
+  for (GradProblem* p : {&pt, &pu}) {
+    p->parts = grad_parts(p->chunks, total1, slots1);
+    p->mode = GRAD_SPLIT;
+    p->P = M;
+    p->R = R;
+    p->half = half;
+  }
+  s1.units0 = pt.tiles * pt.parts;
+  // dA and dB
+  const int slots2 = half == 64 ? 2 * sms : sms;
+  GradProblem &pa = s2.p[0], &pb = s2.p[1];
+  pa.tiles = dA ? (K + 127) / 128 : 0;
+  pa.mode = GRAD_ROWS;
+  pa.P = K;
+  pa.out = static_cast<uint16_t*>(dA);
+  pb.tiles = dB ? N / 128 : 0;
+  pb.mode = GRAD_COLS;
+  pb.P = N;
+  pb.ldo = N;
+  pb.out = static_cast<uint16_t*>(dB);
+  for (GradProblem* p : {&pa, &pb}) {
+    p->a_mn = p->b_mn = 1;
+    p->chunks = mchunks;
+    p->parts = grad_parts(mchunks, static_cast<int64_t>(pa.tiles + pb.tiles) * mchunks, slots2);
+    p->R = R;
+    p->half = half;
+  }
+  s2.units0 = pa.tiles * pa.parts;
+  // dX
+  GradDxParams dx{};
+  dx.dX = static_cast<uint16_t*>(dX);
+  dx.status = h->status;
+  dx.M = M;
+  dx.K = K;
+  dx.chunks = N / 64;
+  dx.rchunks = R > 0 ? 2 * half / 64 : 0;
+  dx.half = half;
+  dx.mt = (M + 255) / 256;
+  dx.kt = (K + 255) / 256;
+  const int tiles = dx.mt * dx.kt;
+  const TileSplit ts = tail_split(tiles, dx.chunks, pairs);
+  dx.full = ts.splits > 1 ? ts.full : tiles;
+  dx.splits = ts.splits;
+  dx.units = dx.full + (tiles - dx.full) * dx.splits;
+  // about as many token tiles as column tiles among those in flight: the fewest operand bytes
+  dx.group = std::max(1, std::min(dx.mt, static_cast<int>(std::lround(std::sqrt(static_cast<double>(pairs))))));
+
+  // scratch, one stream-ordered allocation: [counts][u][t][fp32 parts][dense weight]; the
+  // three launches use the parts' memory one after another
+  const size_t uv = R > 0 ? round256(static_cast<size_t>(M) * 2 * half * sizeof(uint16_t)) : 0;
+  const size_t c1 = static_cast<size_t>(pt.tiles) * 4, c2 = static_cast<size_t>(pu.tiles) * 4;
+  const size_t c3 = static_cast<size_t>(pa.tiles) * 4, c4 = static_cast<size_t>(pb.tiles) * 4;
+  const size_t c5 = dX ? static_cast<size_t>(tiles - dx.full) * 8 : 0;
+  const size_t counts = round256((c1 + c2 + c3 + c4 + c5) * sizeof(uint32_t));
+  const size_t tb = round256(grad_part_bytes(pt, half)), ub = round256(grad_part_bytes(pu, half));
+  const size_t ab = round256(grad_part_bytes(pa, 2 * half)), bb = round256(grad_part_bytes(pb, 2 * half));
+  const size_t xb = dX ? static_cast<size_t>(tiles - dx.full) * dx.splits * 2 * 256 * 128 * sizeof(float) : 0;
+  const size_t parts = std::max(std::max(tb + ub, ab + bb), xb);
+  const size_t dense = dX ? static_cast<size_t>(N) * K * sizeof(uint16_t) : 0;
+  uint8_t* mem = nullptr;
+  SALR_TRY(dev_alloc_async(reinterpret_cast<void**>(&mem), counts + 2 * uv + parts + dense, st,
+                           kPoolScratch));
+  uint32_t* cnt = reinterpret_cast<uint32_t*>(mem);
+  uint16_t* u = reinterpret_cast<uint16_t*>(mem + counts);
+  uint16_t* t = reinterpret_cast<uint16_t*>(mem + counts + uv);
+  uint8_t* pmem = mem + counts + 2 * uv;
+  uint16_t* W = reinterpret_cast<uint16_t*>(pmem + parts);
+  pt.count = cnt;
+  pu.count = cnt + c1;
+  pa.count = cnt + c1 + c2;
+  pb.count = cnt + c1 + c2 + c3;
+  dx.count = cnt + c1 + c2 + c3 + c4;
+  pt.out = t;
+  pu.out = u;
+  pt.part = reinterpret_cast<float*>(pmem);
+  pu.part = reinterpret_cast<float*>(pmem + tb);
+  pa.part = reinterpret_cast<float*>(pmem);
+  pb.part = reinterpret_cast<float*>(pmem + ab);
+  dx.part = reinterpret_cast<float*>(pmem);
+
+  auto run = [&]() -> int {
+    if (counts) SALR_TRY(cudaMemsetAsync(cnt, 0, counts, st));
+    SALR_TRY(apply_wait_limit(st));
+    CUtensorMap m[4];
+    std::memset(m, 0, sizeof(m));
+    int rc = SALR_OK;
+    if (pt.tiles + pu.tiles > 0) {
+      if (pt.tiles && (!make_map(&m[0], X, K, M, 64, 128) || !make_map(&m[1], A_cat, R, K, 64, 64)))
+        return SALR_ERR_CUDA;
+      if (pu.tiles && (!make_map(&m[2], dY, N, M, 64, 128) || !make_map(&m[3], B_cat, N, R, 64, half)))
+        return SALR_ERR_CUDA;
+      rc = half == 64 ? launch_grad_skinny<64>(s1, m, st) : launch_grad_skinny<128>(s1, m, st);
+      if (rc != SALR_OK) return rc;
+    }
+    if (dX) {
+      SALR_TRY(launch_expand(h, W, st));
+      if (!make_map(&m[0], dY, N, M, 64, 128) || !make_map(&m[1], W, K, N, 64, 64)) return SALR_ERR_CUDA;
+      if (R > 0 && (!make_map(&m[2], u, 2 * half, M, 64, 128) || !make_map(&m[3], A_cat, R, K, 64, 128)))
+        return SALR_ERR_CUDA;
+      rc = launch_grad_dx(dx, m, std::min(pairs, dx.units), st);
+      if (rc != SALR_OK) return rc;
+    }
+    if (pa.tiles + pb.tiles > 0) {
+      if (pa.tiles && (!make_map(&m[0], X, K, M, 64, 64) || !make_map(&m[1], u, 2 * half, M, 64, 64)))
+        return SALR_ERR_CUDA;
+      if (pb.tiles && (!make_map(&m[2], dY, N, M, 64, 64) || !make_map(&m[3], t, 2 * half, M, 64, 64)))
+        return SALR_ERR_CUDA;
+      rc = half == 64 ? launch_grad_skinny<128>(s2, m, st) : launch_grad_skinny<256>(s2, m, st);
+    }
+    return rc;
+  };
+  const int rc = run();
+  const cudaError_t e = cudaFreeAsync(mem, st);
+  return rc != SALR_OK ? rc : cuda_status(e);
 }
 
 // ------------------------------------------------------------------------------------

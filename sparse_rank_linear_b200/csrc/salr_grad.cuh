@@ -1,0 +1,611 @@
+// salr_grad.cuh - the gradients of the layer Y = X W^T + (X A) B for a frozen W:
+//
+//     u = dY B^T        dX = dY W + u A^T        dA = X^T u
+//     t = X A                                    dB = t^T dY
+//
+// Three launches after the weight has been expanded to a dense bf16 N x K scratch, all
+// tcgen05 products of operand tiles that TMA brings in as they lie in memory: an operand
+// whose reduction index is its row index is read MN-major (transposed by the tensor core),
+// so nothing is transposed in memory.
+//
+// 1. grad_skinny_kernel, t and u in one launch (two problems): 128 tokens x all ranks per
+//    CTA, the reduction over K or N split over CTAs.  The fp32 result is stored as two bf16
+//    parts side by side, hi = bf16(t) and lo = bf16(t - hi), so that the next products take
+//    t and u to 16 bits of significand and dX, dA and dB carry no rounding but their own.
+// 2. grad_dx_kernel: dX, by pairs of CTAs (cta_group::2).  The u A^T term runs as extra
+//    reduction steps of the same accumulator.
+// 3. grad_skinny_kernel, dA and dB in one launch: 128 rows of K or N x (hi | lo) ranks, the
+//    reduction over tokens split over CTAs; the two halves are added in the epilogue.
+//
+// Parts of a split reduction write their fp32 sums side by side, and the last part of a
+// tile to arrive adds them in order: results repeat bit for bit.
+//
+// Bounds: 2 is tensor-bound (2 M N K flops); 1 and 3 read X and dY once each and are bound
+// by HBM or, when X and dY stay in L2, by L2.
+#pragma once
+#include <cstdint>
+#include <cuda_bf16.h>
+#include "sm100.cuh"
+
+namespace salr {
+
+// ---------------------------------------------------------------- CTA-pair wrappers
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync_all() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The address of shared-memory location `addr` in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t map_to_rank(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+// mbar_wait for a barrier that the other CTA of the pair arrives on.
+__device__ __forceinline__ bool mbar_wait_pair(uint64_t* bar, uint32_t parity) {
+  const uint32_t a = smem_u32(bar);
+  const long long t0 = clock64();
+  for (uint32_t i = 0;; ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(a), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if ((i & 255u) == 255u && clock64() - t0 > wait_limit()) return false;
+  }
+}
+// Tensor copy into this CTA's shared memory that reports to a barrier of either CTA.
+__device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* map, int32_t c0,
+                                                 int32_t c1, uint32_t bar_cluster) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
+      "[%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar_cluster)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t* dst, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)),
+               "r"(ncols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+// D (256 rows, 128 in each CTA's TMEM) (+)= A B^T: each CTA holds its 128 rows of A and its
+// half of B's rows at the same shared-memory offsets.  Issued by the pair's first CTA.
+__device__ __forceinline__ void mma_bf16_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                              uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Arrive on `bar` of both CTAs once every pair MMA issued so far by this thread is done.
+__device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
+
+// ---------------------------------------------------------------- skinny products
+
+constexpr int kGradThreads = 192;  // warp 0 loads, warp 1 issues MMAs, warps 2-5 epilogue
+constexpr int kGradChunk = 64;     // reduction steps per stage
+
+enum : int { GRAD_SPLIT = 0, GRAD_ROWS = 1, GRAD_COLS = 2 };
+
+// C[P x columns] = A-operand (P rows) times B-operand, reduction cut into chunks of 64.
+struct GradProblem {
+  int tiles, parts, chunks;  // row tiles of 128; parts of each tile's reduction; its chunks
+  int a_mn, b_mn;            // operand major: 1 if the reduction index is the row index
+  int mode;  // GRAD_SPLIT: out[p][c] = hi, out[p][half + c] = lo, row length 2 half
+             // GRAD_ROWS:  out[p][c] = column c + column half + c, c < R, row length R
+             // GRAD_COLS:  out[c][p] likewise, row length ldo
+  int P, R, half, ldo;
+  uint16_t* out;
+  float* part;         // [tiles x parts][columns][128], if parts > 1
+  uint32_t* count;     // [tiles][4], zero before the launch
+};
+struct GradSkinnyParams {
+  GradProblem p[2];
+  int units0;  // units (tile, part) of problem 0; the later ones are problem 1's
+  int* status;
+};
+
+struct GradCtrl {
+  uint64_t full[8], empty[8], fin;
+  uint32_t tmem;
+  int abort;
+};
+
+template <int BN>
+struct GradSkinny {
+  static constexpr int kStage = 16384 + BN * 128;
+  // two CTAs an SM up to 128 columns, one with 256
+  static constexpr int kStages = BN == 256 ? 4 : BN == 128 ? 3 : 4;
+  static constexpr int kSmemBytes = kStages * kStage + 1024 + 256;
+};
+
+template <int BN>
+__global__ void __launch_bounds__(kGradThreads)
+    grad_skinny_kernel(const __grid_constant__ GradSkinnyParams prm,
+                       const __grid_constant__ CUtensorMap ma0, const __grid_constant__ CUtensorMap mb0,
+                       const __grid_constant__ CUtensorMap ma1, const __grid_constant__ CUtensorMap mb1) {
+  using L = GradSkinny<BN>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  GradCtrl* ctrl = reinterpret_cast<GradCtrl*>(smem + L::kStages * L::kStage);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int second = static_cast<int>(blockIdx.x) >= prm.units0;
+  const GradProblem& p = prm.p[second];
+  const int unit = blockIdx.x - (second ? prm.units0 : 0);
+  const int tile = unit / p.parts, part = unit % p.parts;
+  const int c0 = static_cast<int>(static_cast<long long>(part) * p.chunks / p.parts);
+  const int c1 = static_cast<int>(static_cast<long long>(part + 1) * p.chunks / p.parts);
+  const int p0 = tile * 128;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < L::kStages; ++s) {
+      mbar_init(&ctrl->full[s], 1);
+      mbar_init(&ctrl->empty[s], 1);
+    }
+    mbar_init(&ctrl->fin, 1);
+    ctrl->abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) tmem_alloc(&ctrl->tmem, BN);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctrl->tmem;
+  volatile int* abort_flag = &ctrl->abort;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      const CUtensorMap* ma = second ? &ma1 : &ma0;
+      const CUtensorMap* mb = second ? &mb1 : &mb0;
+      int s = 0, ph = 0, issued = 0;
+      for (int c = c0; c < c1; ++c) {
+        if (!mbar_wait(&ctrl->empty[s], ph ^ 1) || *abort_flag) {
+          atomicOr(prm.status, DEV_ERR_TIMEOUT);
+          *abort_flag = 1;
+          break;
+        }
+        uint8_t* a = smem + s * L::kStage;
+        uint8_t* b = a + 16384;
+        uint64_t* bar = &ctrl->full[s];
+        mbar_arrive_expect_tx(bar, L::kStage);
+        const int r = c * kGradChunk;
+        if (p.a_mn) {
+          tma_load_2d(a, ma, p0, r, bar);
+          tma_load_2d(a + 8192, ma, p0 + 64, r, bar);
+        } else {
+          tma_load_2d(a, ma, r, p0, bar);
+        }
+        if (p.b_mn) {
+#pragma unroll
+          for (int h = 0; h < BN / 64; ++h) tma_load_2d(b + h * 8192, mb, h * 64, r, bar);
+        } else {
+          tma_load_2d(b, mb, r, 0, bar);
+        }
+        ++issued;
+        if (++s == L::kStages) s = 0, ph ^= 1;
+      }
+      if (*abort_flag)  // let the copies in flight land before the CTA can exit
+        for (int i = issued > L::kStages ? issued - L::kStages : 0; i < issued; ++i)
+          mbar_wait(&ctrl->full[i % L::kStages], (i / L::kStages) & 1);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t idesc = idesc_bf16(128, BN, p.a_mn, p.b_mn);
+      // per 16 reduction steps: 32 bytes along a K-major row, 16 rows of an MN-major tile
+      const uint32_t astep = p.a_mn ? 2048 : 32, bstep = p.b_mn ? 2048 : 32;
+      const uint32_t albo = p.a_mn ? 8192 : 16, blbo = p.b_mn ? 8192 : 16;
+      int s = 0, ph = 0;
+      for (int c = c0; c < c1; ++c) {
+        if (!mbar_wait(&ctrl->full[s], ph) || *abort_flag) {
+          atomicOr(prm.status, DEV_ERR_TIMEOUT);
+          *abort_flag = 1;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t a = smem_u32(smem + s * L::kStage), b = a + 16384;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          mma_bf16_ss(tmem, smem_desc_sw128(a + astep * k, albo, 1024),
+                      smem_desc_sw128(b + bstep * k, blbo, 1024), idesc, c != c0 || k != 0);
+        mma_commit(&ctrl->empty[s]);
+        if (++s == L::kStages) s = 0, ph ^= 1;
+      }
+      mma_commit(&ctrl->fin);
+      if (!mbar_wait(&ctrl->fin, 0)) atomicOr(prm.status, DEV_ERR_TIMEOUT);
+    }
+  } else {
+    const int q = warp & 3;  // TMEM lane quarter
+    const int row = 32 * q + lane;
+    const uint32_t tm = tmem + (static_cast<uint32_t>(32 * q) << 16);
+    const bool ok = mbar_wait(&ctrl->fin, 0) && !*abort_flag;
+    if (__all_sync(0xffffffffu, ok)) {
+      tc_fence_after();
+      bool mine = true;  // this warp finishes its rows
+      float* parts = p.part + static_cast<size_t>(tile) * p.parts * BN * 128 + row;
+      if (p.parts > 1) {
+        float* dst = parts + static_cast<size_t>(part) * BN * 128;
+        for (int c = 0; c < BN; c += 16) {
+          uint32_t v[16];
+          tmem_ld16(tm + c, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 16; ++e) __stcg(dst + (c + e) * 128, __uint_as_float(v[e]));
+        }
+        __threadfence();
+        __syncwarp();
+        uint32_t last = 0;
+        if (lane == 0) last = atomicAdd(p.count + tile * 4 + q, 1u) == static_cast<uint32_t>(p.parts - 1);
+        mine = __shfl_sync(0xffffffffu, last, 0) != 0;
+        if (mine) __threadfence();
+      }
+      // 16 columns of this thread's row: from TMEM, or the parts' sum in order
+      auto load16 = [&](int c, float (&v)[16]) {
+        if (p.parts == 1) {
+          uint32_t w[16];
+          tmem_ld16(tm + c, w);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(w[e]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) v[e] = 0.f;
+          for (int k = 0; k < p.parts; ++k) {
+            const float* src = parts + (static_cast<size_t>(k) * BN + c) * 128;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) v[e] += __ldcg(src + e * 128);
+          }
+        }
+      };
+      if (mine) {
+        const size_t pr = static_cast<size_t>(p0) + row;
+        const bool live = p0 + row < p.P;
+        auto pack = [](float a, float b) {
+          const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+          return *reinterpret_cast<const uint32_t*>(&h);
+        };
+        if (p.mode == GRAD_SPLIT) {
+          for (int c = 0; c < BN; c += 16) {
+            float v[16];
+            load16(c, v);
+            uint32_t hi[8], lo[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              hi[e] = pack(v[2 * e], v[2 * e + 1]);
+              const float h0 = __uint_as_float(hi[e] << 16), h1 = __uint_as_float(hi[e] & 0xffff0000u);
+              // an infinite value is all in hi
+              lo[e] = pack(fabsf(h0) <= 3.38953139e38f ? v[2 * e] - h0 : 0.f,
+                           fabsf(h1) <= 3.38953139e38f ? v[2 * e + 1] - h1 : 0.f);
+            }
+            if (live) {
+              uint4* o = reinterpret_cast<uint4*>(p.out + pr * 2 * p.half + c);
+              o[0] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+              o[1] = make_uint4(hi[4], hi[5], hi[6], hi[7]);
+              o = reinterpret_cast<uint4*>(p.out + pr * 2 * p.half + p.half + c);
+              o[0] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+              o[1] = make_uint4(lo[4], lo[5], lo[6], lo[7]);
+            }
+          }
+        } else {
+          for (int c = 0; c < p.R; c += 16) {
+            float v[16], w[16];
+            load16(c, v);
+            load16(p.half + c, w);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) v[e] += w[e];
+            if (!live) continue;
+            if (p.mode == GRAD_ROWS) {
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+                if (c + 8 * h < p.R)
+                  *reinterpret_cast<uint4*>(p.out + pr * p.R + c + 8 * h) =
+                      make_uint4(pack(v[8 * h], v[8 * h + 1]), pack(v[8 * h + 2], v[8 * h + 3]),
+                                 pack(v[8 * h + 4], v[8 * h + 5]), pack(v[8 * h + 6], v[8 * h + 7]));
+            } else {
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                if (c + e < p.R)
+                  reinterpret_cast<__nv_bfloat16*>(p.out)[static_cast<size_t>(c + e) * p.ldo + pr] =
+                      __float2bfloat16_rn(v[e]);
+            }
+          }
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, BN);
+  }
+}
+
+// ---------------------------------------------------------------- dX
+
+// dX[M x K] in tiles of 256 tokens x 256 columns, a pair of CTAs each: a CTA loads its 128
+// tokens of dY and its 128 columns of W per step of 64 (32 KB, half of what a lone CTA would
+// load per flop), the first CTA issues the MMAs for both, and each keeps its 128 x 256 half
+// of the accumulator in its own TMEM, twice, so that the epilogue of a tile overlaps the
+// next one.  Persistent; the tiles of a last, partial round are split along N.
+constexpr int kDxStages = 6;
+constexpr int kDxStage = 32768;
+
+struct GradDxParams {
+  uint16_t* dX;
+  float* part;      // [split tiles][parts][2 CTAs][256 columns][128 rows]
+  uint32_t* count;  // [split tiles][2][4], zero before the launch
+  int* status;
+  int M, K;
+  int chunks;       // N / 64
+  int rchunks;      // steps of u A^T: (hi, lo) x ranks / 64, or 0
+  int half;         // columns of hi in u
+  int mt, kt;       // tiles of 256 tokens, of 256 columns
+  int full, splits, units;  // whole tiles; parts of each later tile; units in all
+  int group;        // token tiles that go together, column tile by column tile
+};
+
+struct GradDxUnit {
+  int st, part, parts, m, k, c0, nc, nr;  // st: index among the split tiles
+};
+__device__ __forceinline__ GradDxUnit grad_dx_unit(const GradDxParams& p, int u) {
+  GradDxUnit w;
+  int t;
+  const int nsu = p.units - p.full;  // the parts of split tiles come first
+  if (u >= nsu) {
+    t = u - nsu;
+    w.st = w.part = 0;
+    w.parts = 1;
+  } else {
+    w.st = u / p.splits;
+    t = p.full + w.st;
+    w.part = u % p.splits;
+    w.parts = p.splits;
+  }
+  const int per = p.group * p.kt, g = t / per, r = t - g * per;
+  const int rows = min(p.group, p.mt - g * p.group);
+  w.m = g * p.group + r % rows;
+  w.k = r / rows;
+  w.c0 = static_cast<int>(static_cast<long long>(w.part) * p.chunks / w.parts);
+  w.nc = static_cast<int>(static_cast<long long>(w.part + 1) * p.chunks / w.parts) - w.c0;
+  w.nr = w.part == 0 ? p.rchunks : 0;
+  return w;
+}
+
+struct GradDxCtrl {
+  uint64_t full[kDxStages], empty[kDxStages];
+  uint64_t accfull[2], accempty[2], fin;
+  uint32_t tmem;
+  int abort;
+};
+constexpr int kDxSmemBytes = kDxStages * kDxStage + 1024 + 256;
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
+    grad_dx_kernel(const __grid_constant__ GradDxParams p, const __grid_constant__ CUtensorMap mdy,
+                   const __grid_constant__ CUtensorMap mw, const __grid_constant__ CUtensorMap mu,
+                   const __grid_constant__ CUtensorMap ma) {
+  extern __shared__ uint8_t smem_raw[];
+  // the same offset in both CTAs: dynamic shared memory starts alike in every CTA
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  GradDxCtrl* ctrl = reinterpret_cast<GradDxCtrl*>(smem + kDxStages * kDxStage);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kDxStages; ++s) {
+      mbar_init(&ctrl->full[s], 1);
+      mbar_init(&ctrl->empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&ctrl->accfull[b], 1);
+      mbar_init(&ctrl->accempty[b], 8);  // the epilogue warps of both CTAs
+    }
+    mbar_init(&ctrl->fin, 1);
+    ctrl->abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) tmem_alloc_pair(&ctrl->tmem, 512);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem = ctrl->tmem;
+  volatile int* abort_flag = &ctrl->abort;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int s = 0, ph = 0;
+      long long issued = 0;
+      bool ok = true;
+      for (int u = pair; u < p.units && ok; u += pairs) {
+        const GradDxUnit w = grad_dx_unit(p, u);
+        const int row = w.m * 256 + static_cast<int>(rank) * 128;
+        const int col = w.k * 256 + static_cast<int>(rank) * 128;
+        for (int c = 0; c < w.nc + w.nr; ++c) {
+          if (!mbar_wait_pair(&ctrl->empty[s], ph ^ 1) || *abort_flag) {
+            atomicOr(p.status, DEV_ERR_TIMEOUT);
+            *abort_flag = 1;
+            ok = false;
+            break;
+          }
+          // both CTAs' copies count on the first CTA's barrier
+          if (rank == 0) mbar_arrive_expect_tx(&ctrl->full[s], 2 * kDxStage);
+          const uint32_t bar = map_to_rank(smem_u32(&ctrl->full[s]), 0);
+          uint8_t* a = smem + s * kDxStage;
+          uint8_t* b = a + 16384;
+          if (c < w.nc) {
+            const int n = (w.c0 + c) * kGradChunk;
+            tma_load_2d_pair(a, &mdy, n, row, bar);
+            tma_load_2d_pair(b, &mw, col, n, bar);
+            tma_load_2d_pair(b + 8192, &mw, col + 64, n, bar);
+          } else {
+            const int r = (c - w.nc) * kGradChunk;
+            tma_load_2d_pair(a, &mu, r, row, bar);
+            tma_load_2d_pair(b, &ma, r >= p.half ? r - p.half : r, col, bar);
+          }
+          ++issued;
+          if (++s == kDxStages) s = 0, ph ^= 1;
+        }
+      }
+      if (*abort_flag) {
+        // let the copies in flight land before the CTAs can exit: the first CTA's barriers
+        // count both CTAs' bytes, and the second CTA stays until the first one is through
+        if (rank == 0)
+          for (long long i = issued > kDxStages ? issued - kDxStages : 0; i < issued; ++i)
+            mbar_wait_pair(&ctrl->full[i % kDxStages], (i / kDxStages) & 1);
+        for (int i = 0; i < 100; ++i) __nanosleep(1000);
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      constexpr uint32_t idesc_w = idesc_bf16(256, 256, 0, 1), idesc_r = idesc_bf16(256, 256, 0, 0);
+      int s = 0, ph = 0, t = 0;
+      bool ok = true;
+      for (int u = pair; u < p.units && ok; u += pairs, ++t) {
+        const GradDxUnit w = grad_dx_unit(p, u);
+        const int b = t & 1;
+        const uint32_t acc = tmem + b * 256;
+        if (!mbar_wait_pair(&ctrl->accempty[b], ((t >> 1) & 1) ^ 1) || *abort_flag) {
+          atomicOr(p.status, DEV_ERR_TIMEOUT);
+          *abort_flag = 1;
+          break;
+        }
+        tc_fence_after();
+        for (int c = 0; c < w.nc + w.nr; ++c) {
+          if (!mbar_wait_pair(&ctrl->full[s], ph) || *abort_flag) {
+            atomicOr(p.status, DEV_ERR_TIMEOUT);
+            *abort_flag = 1;
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a0 = smem_u32(smem + s * kDxStage), b0 = a0 + 16384;
+          if (c < w.nc) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma_bf16_pair(acc, smem_desc_sw128(a0 + 32 * k, 16, 1024),
+                            smem_desc_sw128(b0 + 2048 * k, 8192, 1024), idesc_w, c != 0 || k != 0);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma_bf16_pair(acc, smem_desc_sw128(a0 + 32 * k, 16, 1024),
+                            smem_desc_sw128(b0 + 32 * k, 16, 1024), idesc_r, 1u);
+          }
+          mma_commit_pair(&ctrl->empty[s]);
+          if (++s == kDxStages) s = 0, ph ^= 1;
+        }
+        if (ok) mma_commit_pair(&ctrl->accfull[b]);
+      }
+      mma_commit_pair(&ctrl->fin);
+    }
+  } else {
+    const int q = warp & 3;
+    const int row = 32 * q + lane;
+    int t = 0;
+    for (int u = pair; u < p.units; u += pairs, ++t) {
+      const GradDxUnit w = grad_dx_unit(p, u);
+      const int b = t & 1;
+      const uint32_t tm = tmem + b * 256 + (static_cast<uint32_t>(32 * q) << 16);
+      const bool ok = mbar_wait_pair(&ctrl->accfull[b], (t >> 1) & 1) && !*abort_flag;
+      if (!ok) {
+        atomicOr(p.status, DEV_ERR_TIMEOUT);
+        *abort_flag = 1;
+      }
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc_fence_after();
+      const size_t m = static_cast<size_t>(w.m) * 256 + rank * 128 + row;
+      const int k0 = w.k * 256, kn = min(256, p.K - k0);
+      uint16_t* out = p.dX + m * p.K + k0;
+      const bool live = m < static_cast<size_t>(p.M);
+      auto store16 = [&](int c, const float (&v)[16]) {
+        uint32_t h[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const __nv_bfloat162 x = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
+          h[e] = *reinterpret_cast<const uint32_t*>(&x);
+        }
+        if (live) {
+          uint4* o = reinterpret_cast<uint4*>(out + c);
+          o[0] = make_uint4(h[0], h[1], h[2], h[3]);
+          o[1] = make_uint4(h[4], h[5], h[6], h[7]);
+        }
+      };
+      float* parts = p.part + (static_cast<size_t>(w.st) * w.parts * 2 + rank) * 256 * 128 + row;
+      constexpr size_t kPartStride = 2 * 256 * 128;
+      for (int c = 0; c < kn; c += 16) {
+        uint32_t x[16];
+        float v[16];
+        tmem_ld16(tm + c, x);
+        tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(x[e]);
+        if (w.parts == 1) {
+          store16(c, v);
+        } else {
+          float* dst = parts + w.part * kPartStride + c * 128;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) __stcg(dst + e * 128, v[e]);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_u32(&ctrl->accempty[b]), 0));
+      if (w.parts > 1) {
+        __threadfence();
+        __syncwarp();
+        uint32_t last = 0;
+        if (lane == 0)
+          last = atomicAdd(p.count + (w.st * 2 + rank) * 4 + q, 1u) == static_cast<uint32_t>(w.parts - 1);
+        if (__shfl_sync(0xffffffffu, last, 0)) {
+          __threadfence();
+          for (int c = 0; c < kn; c += 16) {
+            float v[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) v[e] = 0.f;
+            for (int k = 0; k < w.parts; ++k) {
+              const float* src = parts + k * kPartStride + c * 128;
+#pragma unroll
+              for (int e = 0; e < 16; ++e) v[e] += __ldcg(src + e * 128);
+            }
+            store16(c, v);
+          }
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  // the last signal to this CTA's barriers has arrived, and then
+  if (warp == 1 && lane == 0 && !mbar_wait_pair(&ctrl->fin, 0)) atomicOr(p.status, DEV_ERR_TIMEOUT);
+  __syncwarp();
+  cluster_sync_all();  // neither CTA leaves while the other may still signal or read it
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+}  // namespace salr
