@@ -394,7 +394,7 @@ SALR_API int salr_q4_encode(const void* W, int64_t N, int64_t K, int64_t group, 
  * bf16 rounding that salr_decode gives.  Each output is rounded once, and results repeat
  * bit for bit.
  *
- * Two to four kernels and a memset, with scratch from the library's pool taken on `stream`
+ * One to four kernels (and a memset where tiles of dX are split), with scratch from the library's pool taken on `stream`
  * and given back to it in stream order: with dX the dense weight (2 N K bytes), and 8 to 16
  * bytes per token and rank.  Nothing of the handle is written but its status word, so calls
  * on one handle may run concurrently on several streams; captured, a call keeps its scratch

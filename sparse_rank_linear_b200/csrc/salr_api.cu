@@ -1426,11 +1426,31 @@ int salr_load(const void* buf, int64_t buf_bytes, void* stream, salr_handle* out
 // ------------------------------------------------------------------------------------
 namespace {
 
-// Parts of each tile's reduction, so that `slots` CTAs share `total` chunks evenly; a part
-// keeps at least 8 chunks (its fp32 sum costs a write and a read in L2).
-int grad_parts(int chunks, int64_t total, int slots) {
-  const int64_t each = std::max<int64_t>(8, (total + slots - 1) / slots);
-  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(chunks, (chunks + each - 1) / each)));
+// CTAs that share a row tile's reduction (a cluster): the largest power of two up to 8 that
+// leaves all CTAs resident at once.
+int grad_cluster(int tiles, int slots) {
+  int c = 1;
+  while (c < 8 && tiles * c * 2 <= slots) c *= 2;
+  return c;
+}
+
+// Work split of the dX kernel: whole tiles in full rounds of the pairs, and the tiles of a
+// last, partial round in s parts each along the reduction of kb chunks.  A split costs its
+// fp32 sums' way through L2 and the last part's adding up, about kDxSplitCost chunks' time
+// for the round.
+constexpr int kDxSplitCost = 24;
+TileSplit dx_split(int tiles, int kb, int pairs) {
+  const int rem = tiles % pairs;
+  TileSplit r{tiles, 1};
+  long long best = kb;
+  for (int s = 2; s <= kDxMaxParts && rem > 0 && kb / s >= 8; ++s) {
+    const long long cost = (static_cast<long long>(rem) * s + pairs - 1) / pairs * ((kb + s - 1) / s) + kDxSplitCost;
+    if (cost < best) {
+      best = cost;
+      r = TileSplit{tiles - rem, s};
+    }
+  }
+  return r;
 }
 
 template <int BN>
@@ -1444,9 +1464,20 @@ int launch_grad_skinny(const GradSkinnyParams& p, const CUtensorMap* m, cudaStre
                                   GradSkinny<BN>::kSmemBytes));
     attr_set[dev] = true;
   }
-  const unsigned grid = static_cast<unsigned>(p.units0 + p.p[1].tiles * p.p[1].parts);
-  grad_skinny_kernel<BN><<<grid, kGradThreads, GradSkinny<BN>::kSmemBytes, st>>>(p, m[0], m[1], m[2], m[3]);
-  SALR_TRY(cudaGetLastError());
+  const int tiles = p.p[0].tiles + p.p[1].tiles;
+  const int nc = grad_cluster(tiles, (BN == 256 ? 1 : 2) * device_sms(dev));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles * nc));
+  cfg.blockDim = dim3(kGradThreads);
+  cfg.dynamicSmemBytes = GradSkinny<BN>::kSmemBytes;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(nc);
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  SALR_TRY(cudaLaunchKernelEx(&cfg, grad_skinny_kernel<BN>, p, nc, m[0], m[1], m[2], m[3]));
   return SALR_OK;
 }
 
@@ -1462,10 +1493,6 @@ int launch_grad_dx(const GradDxParams& p, const CUtensorMap* m, int pairs, cudaS
   grad_dx_kernel<<<2 * pairs, kGradThreads, kDxSmemBytes, st>>>(p, m[0], m[1], m[2], m[3]);
   SALR_TRY(cudaGetLastError());
   return SALR_OK;
-}
-
-size_t grad_part_bytes(const GradProblem& p, int columns) {
-  return p.parts > 1 ? static_cast<size_t>(p.tiles) * p.parts * columns * 128 * sizeof(float) : 0;
 }
 
 }  // namespace
@@ -1489,14 +1516,12 @@ int salr_linear_backward(const void* dY, const void* X, int64_t M64, salr_handle
   const int M = static_cast<int>(M64), N = static_cast<int>(h->N), K = static_cast<int>(h->K);
   const int R = static_cast<int>(R64), half = R <= 64 ? 64 : 128;
   const int sms = device_sms(h->device), pairs = std::max(1, sms / 2);
-  const int mtiles = (M + 127) / 128, mchunks = (M + 63) / 64;
+  const int mtiles = (M + 127) / 128;
   const bool want_u = R > 0 && (dX || dA), want_t = dB != nullptr;
 
   // t and u
   GradSkinnyParams s1{}, s2{};
   s1.status = s2.status = h->status;
-  const int slots1 = 2 * sms;
-  const int64_t total1 = static_cast<int64_t>(mtiles) * ((want_t ? K / 64 : 0) + (want_u ? N / 64 : 0));
   GradProblem &pt = s1.p[0], &pu = s1.p[1];
   pt.tiles = want_t ? mtiles : 0;
   pt.chunks = K / 64;
@@ -1504,15 +1529,12 @@ int salr_linear_backward(const void* dY, const void* X, int64_t M64, salr_handle
   pu.tiles = want_u ? mtiles : 0;
   pu.chunks = N / 64;
   for (GradProblem* p : {&pt, &pu}) {
-    p->parts = grad_parts(p->chunks, total1, slots1);
     p->mode = GRAD_SPLIT;
     p->P = M;
     p->R = R;
     p->half = half;
   }
-  s1.units0 = pt.tiles * pt.parts;
   // dA and dB
-  const int slots2 = half == 64 ? 2 * sms : sms;
   GradProblem &pa = s2.p[0], &pb = s2.p[1];
   pa.tiles = dA ? (K + 127) / 128 : 0;
   pa.mode = GRAD_ROWS;
@@ -1525,12 +1547,10 @@ int salr_linear_backward(const void* dY, const void* X, int64_t M64, salr_handle
   pb.out = static_cast<uint16_t*>(dB);
   for (GradProblem* p : {&pa, &pb}) {
     p->a_mn = p->b_mn = 1;
-    p->chunks = mchunks;
-    p->parts = grad_parts(mchunks, static_cast<int64_t>(pa.tiles + pb.tiles) * mchunks, slots2);
+    p->chunks = (M + 63) / 64;
     p->R = R;
     p->half = half;
   }
-  s2.units0 = pa.tiles * pa.parts;
   // dX
   GradDxParams dx{};
   dx.dX = static_cast<uint16_t*>(dX);
@@ -1543,24 +1563,18 @@ int salr_linear_backward(const void* dY, const void* X, int64_t M64, salr_handle
   dx.mt = (M + 255) / 256;
   dx.kt = (K + 255) / 256;
   const int tiles = dx.mt * dx.kt;
-  const TileSplit ts = tail_split(tiles, dx.chunks, pairs);
-  dx.full = ts.splits > 1 ? ts.full : tiles;
+  const TileSplit ts = dx_split(tiles, dx.chunks, pairs);
+  dx.full = ts.full;
   dx.splits = ts.splits;
   dx.units = dx.full + (tiles - dx.full) * dx.splits;
   // about as many token tiles as column tiles among those in flight: the fewest operand bytes
   dx.group = std::max(1, std::min(dx.mt, static_cast<int>(std::lround(std::sqrt(static_cast<double>(pairs))))));
 
-  // scratch, one stream-ordered allocation: [counts][u][t][fp32 parts][dense weight]; the
-  // three launches use the parts' memory one after another
+  // scratch, one stream-ordered allocation: [dX counts][u][t][dX fp32 parts][dense weight]
   const size_t uv = R > 0 ? round256(static_cast<size_t>(M) * 2 * half * sizeof(uint16_t)) : 0;
-  const size_t c1 = static_cast<size_t>(pt.tiles) * 4, c2 = static_cast<size_t>(pu.tiles) * 4;
-  const size_t c3 = static_cast<size_t>(pa.tiles) * 4, c4 = static_cast<size_t>(pb.tiles) * 4;
-  const size_t c5 = dX ? static_cast<size_t>(tiles - dx.full) * 8 : 0;
-  const size_t counts = round256((c1 + c2 + c3 + c4 + c5) * sizeof(uint32_t));
-  const size_t tb = round256(grad_part_bytes(pt, half)), ub = round256(grad_part_bytes(pu, half));
-  const size_t ab = round256(grad_part_bytes(pa, 2 * half)), bb = round256(grad_part_bytes(pb, 2 * half));
-  const size_t xb = dX ? static_cast<size_t>(tiles - dx.full) * dx.splits * 2 * 256 * 128 * sizeof(float) : 0;
-  const size_t parts = std::max(std::max(tb + ub, ab + bb), xb);
+  const size_t split_tiles = dX ? static_cast<size_t>(tiles - dx.full) : 0;
+  const size_t counts = round256(split_tiles * 8 * sizeof(uint32_t));
+  const size_t parts = split_tiles * dx.splits * 2 * 256 * 128 * sizeof(float);
   const size_t dense = dX ? static_cast<size_t>(N) * K * sizeof(uint16_t) : 0;
   uint8_t* mem = nullptr;
   SALR_TRY(dev_alloc_async(reinterpret_cast<void**>(&mem), counts + 2 * uv + parts + dense, st,
@@ -1568,20 +1582,11 @@ int salr_linear_backward(const void* dY, const void* X, int64_t M64, salr_handle
   uint32_t* cnt = reinterpret_cast<uint32_t*>(mem);
   uint16_t* u = reinterpret_cast<uint16_t*>(mem + counts);
   uint16_t* t = reinterpret_cast<uint16_t*>(mem + counts + uv);
-  uint8_t* pmem = mem + counts + 2 * uv;
-  uint16_t* W = reinterpret_cast<uint16_t*>(pmem + parts);
-  pt.count = cnt;
-  pu.count = cnt + c1;
-  pa.count = cnt + c1 + c2;
-  pb.count = cnt + c1 + c2 + c3;
-  dx.count = cnt + c1 + c2 + c3 + c4;
+  uint16_t* W = reinterpret_cast<uint16_t*>(mem + counts + 2 * uv + parts);
+  dx.count = cnt;
+  dx.part = reinterpret_cast<float*>(mem + counts + 2 * uv);
   pt.out = t;
   pu.out = u;
-  pt.part = reinterpret_cast<float*>(pmem);
-  pu.part = reinterpret_cast<float*>(pmem + tb);
-  pa.part = reinterpret_cast<float*>(pmem);
-  pb.part = reinterpret_cast<float*>(pmem + ab);
-  dx.part = reinterpret_cast<float*>(pmem);
 
   auto run = [&]() -> int {
     if (counts) SALR_TRY(cudaMemsetAsync(cnt, 0, counts, st));

@@ -17,8 +17,7 @@
 // 3. grad_skinny_kernel, dA and dB in one launch: 128 rows of K or N x (hi | lo) ranks, the
 //    reduction over tokens split over CTAs; the two halves are added in the epilogue.
 //
-// Parts of a split reduction write their fp32 sums side by side, and the last part of a
-// tile to arrive adds them in order: results repeat bit for bit.
+// Parts of a split reduction are added up in a fixed order: results repeat bit for bit.
 //
 // Bounds: 2 is tensor-bound (2 M N K flops); 1 and 3 read X and dY once each and are bound
 // by HBM or, when X and dY stay in L2, by L2.
@@ -110,24 +109,21 @@ enum : int { GRAD_SPLIT = 0, GRAD_ROWS = 1, GRAD_COLS = 2 };
 
 // C[P x columns] = A-operand (P rows) times B-operand, reduction cut into chunks of 64.
 struct GradProblem {
-  int tiles, parts, chunks;  // row tiles of 128; parts of each tile's reduction; its chunks
-  int a_mn, b_mn;            // operand major: 1 if the reduction index is the row index
+  int tiles, chunks;  // row tiles of 128; chunks of the reduction
+  int a_mn, b_mn;     // operand major: 1 if the reduction index is the row index
   int mode;  // GRAD_SPLIT: out[p][c] = hi, out[p][half + c] = lo, row length 2 half
              // GRAD_ROWS:  out[p][c] = column c + column half + c, c < R, row length R
              // GRAD_COLS:  out[c][p] likewise, row length ldo
   int P, R, half, ldo;
   uint16_t* out;
-  float* part;         // [tiles x parts][columns][128], if parts > 1
-  uint32_t* count;     // [tiles][4], zero before the launch
 };
 struct GradSkinnyParams {
   GradProblem p[2];
-  int units0;  // units (tile, part) of problem 0; the later ones are problem 1's
   int* status;
 };
 
 struct GradCtrl {
-  uint64_t full[8], empty[8], fin;
+  uint64_t full[4], empty[4], fin;
   uint32_t tmem;
   int abort;
 };
@@ -136,27 +132,42 @@ template <int BN>
 struct GradSkinny {
   static constexpr int kStage = 16384 + BN * 128;
   // two CTAs an SM up to 128 columns, one with 256
-  static constexpr int kStages = BN == 256 ? 4 : BN == 128 ? 3 : 4;
+  static constexpr int kStages = BN == 128 ? 3 : 4;
   static constexpr int kSmemBytes = kStages * kStage + 1024 + 256;
+  static_assert(kStages * kStage >= BN * 512, "the stages hold the fp32 sums at the end");
 };
 
+// One float of shared memory of a CTA of the cluster.
+__device__ __forceinline__ float ld_cluster(uint32_t cluster_addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr));
+  return v;
+}
+
+// A cluster of `nc` CTAs (1 to 8) takes a row tile, each CTA a part of its reduction.  The
+// parts' fp32 sums then lie in the CTAs' shared memory ([column][row], where the stages
+// were), and each CTA adds up and writes 128 / nc of the rows, in the order of the parts.
+// Parts that met in L2 instead, added up by the last one to arrive, spent most of the time
+// in that one CTA's chain of L2 reads: up_proj M = 2048 took 60 + 65 us for the two
+// launches.
 template <int BN>
 __global__ void __launch_bounds__(kGradThreads)
-    grad_skinny_kernel(const __grid_constant__ GradSkinnyParams prm,
+    grad_skinny_kernel(const __grid_constant__ GradSkinnyParams prm, const int nc,
                        const __grid_constant__ CUtensorMap ma0, const __grid_constant__ CUtensorMap mb0,
                        const __grid_constant__ CUtensorMap ma1, const __grid_constant__ CUtensorMap mb1) {
   using L = GradSkinny<BN>;
   extern __shared__ uint8_t smem_raw[];
+  // the same offset in every CTA: dynamic shared memory starts alike in all of them
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   GradCtrl* ctrl = reinterpret_cast<GradCtrl*>(smem + L::kStages * L::kStage);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int second = static_cast<int>(blockIdx.x) >= prm.units0;
+  const int part = blockIdx.x % nc, all = blockIdx.x / nc;
+  const int second = all >= prm.p[0].tiles;
   const GradProblem& p = prm.p[second];
-  const int unit = blockIdx.x - (second ? prm.units0 : 0);
-  const int tile = unit / p.parts, part = unit % p.parts;
-  const int c0 = static_cast<int>(static_cast<long long>(part) * p.chunks / p.parts);
-  const int c1 = static_cast<int>(static_cast<long long>(part + 1) * p.chunks / p.parts);
+  const int tile = all - (second ? prm.p[0].tiles : 0);
+  const int c0 = static_cast<int>(static_cast<long long>(part) * p.chunks / nc);
+  const int c1 = static_cast<int>(static_cast<long long>(part + 1) * p.chunks / nc);
   const int p0 = tile * 128;
 
   if (threadIdx.x == 0) {
@@ -233,109 +244,95 @@ __global__ void __launch_bounds__(kGradThreads)
         if (++s == L::kStages) s = 0, ph ^= 1;
       }
       mma_commit(&ctrl->fin);
-      if (!mbar_wait(&ctrl->fin, 0)) atomicOr(prm.status, DEV_ERR_TIMEOUT);
-    }
-  } else {
-    const int q = warp & 3;  // TMEM lane quarter
-    const int row = 32 * q + lane;
-    const uint32_t tm = tmem + (static_cast<uint32_t>(32 * q) << 16);
-    const bool ok = mbar_wait(&ctrl->fin, 0) && !*abort_flag;
-    if (__all_sync(0xffffffffu, ok)) {
-      tc_fence_after();
-      bool mine = true;  // this warp finishes its rows
-      float* parts = p.part + static_cast<size_t>(tile) * p.parts * BN * 128 + row;
-      if (p.parts > 1) {
-        float* dst = parts + static_cast<size_t>(part) * BN * 128;
-        for (int c = 0; c < BN; c += 16) {
-          uint32_t v[16];
-          tmem_ld16(tm + c, v);
-          tmem_ld_wait();
-#pragma unroll
-          for (int e = 0; e < 16; ++e) __stcg(dst + (c + e) * 128, __uint_as_float(v[e]));
-        }
-        __threadfence();
-        __syncwarp();
-        uint32_t last = 0;
-        if (lane == 0) last = atomicAdd(p.count + tile * 4 + q, 1u) == static_cast<uint32_t>(p.parts - 1);
-        mine = __shfl_sync(0xffffffffu, last, 0) != 0;
-        if (mine) __threadfence();
+      if (!mbar_wait(&ctrl->fin, 0)) {
+        atomicOr(prm.status, DEV_ERR_TIMEOUT);
+        *abort_flag = 1;
       }
-      // 16 columns of this thread's row: from TMEM, or the parts' sum in order
-      auto load16 = [&](int c, float (&v)[16]) {
-        if (p.parts == 1) {
-          uint32_t w[16];
-          tmem_ld16(tm + c, w);
-          tmem_ld_wait();
+    }
+  }
+  __syncthreads();  // every product is in TMEM, and the stages are free
+  const bool ok = *abort_flag == 0;
+  float* sums = reinterpret_cast<float*>(smem);  // [BN][128]
+  if (warp >= 2 && ok) {
+    const int q = warp & 3;  // TMEM lane quarter
+    const uint32_t tm = tmem + (static_cast<uint32_t>(32 * q) << 16);
+    tc_fence_after();
+    for (int c = 0; c < BN; c += 16) {
+      uint32_t v[16];
+      tmem_ld16(tm + c, v);
+      tmem_ld_wait();
 #pragma unroll
-          for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(w[e]);
-        } else {
+      for (int e = 0; e < 16; ++e)  // an empty part adds nothing
+        sums[(c + e) * 128 + 32 * q + lane] = c1 > c0 ? __uint_as_float(v[e]) : 0.f;
+    }
+    tc_fence_before();
+  }
+  __syncthreads();
+  cluster_sync_all();
+  if (warp >= 2 && ok) {
+    const int rows = 128 / nc, tid = threadIdx.x - 64;
+    const int row = part * rows + tid % rows, group = tid / rows;  // nc groups of columns
+    const uint32_t base = smem_u32(sums + row);
+    uint32_t from[8];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) v[e] = 0.f;
-          for (int k = 0; k < p.parts; ++k) {
-            const float* src = parts + (static_cast<size_t>(k) * BN + c) * 128;
+    for (int k = 0; k < 8; ++k) from[k] = map_to_rank(base, k < nc ? k : 0);
+    auto load8 = [&](int c, float (&v)[8]) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) v[e] += __ldcg(src + e * 128);
-          }
+      for (int e = 0; e < 8; ++e) v[e] = 0.f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (k < nc) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] += ld_cluster(from[k] + (c + e) * 512);
         }
-      };
-      if (mine) {
-        const size_t pr = static_cast<size_t>(p0) + row;
-        const bool live = p0 + row < p.P;
-        auto pack = [](float a, float b) {
-          const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-          return *reinterpret_cast<const uint32_t*>(&h);
-        };
-        if (p.mode == GRAD_SPLIT) {
-          for (int c = 0; c < BN; c += 16) {
-            float v[16];
-            load16(c, v);
-            uint32_t hi[8], lo[8];
+    };
+    auto pack = [](float a, float b) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+      return *reinterpret_cast<const uint32_t*>(&h);
+    };
+    const size_t pr = static_cast<size_t>(p0) + row;
+    const bool live = p0 + row < p.P;
+    if (p.mode == GRAD_SPLIT) {
+      for (int c = 8 * group; c < BN; c += 8 * nc) {
+        float v[8];
+        load8(c, v);
+        uint32_t hi[4], lo[4];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              hi[e] = pack(v[2 * e], v[2 * e + 1]);
-              const float h0 = __uint_as_float(hi[e] << 16), h1 = __uint_as_float(hi[e] & 0xffff0000u);
-              // an infinite value is all in hi
-              lo[e] = pack(fabsf(h0) <= 3.38953139e38f ? v[2 * e] - h0 : 0.f,
-                           fabsf(h1) <= 3.38953139e38f ? v[2 * e + 1] - h1 : 0.f);
-            }
-            if (live) {
-              uint4* o = reinterpret_cast<uint4*>(p.out + pr * 2 * p.half + c);
-              o[0] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-              o[1] = make_uint4(hi[4], hi[5], hi[6], hi[7]);
-              o = reinterpret_cast<uint4*>(p.out + pr * 2 * p.half + p.half + c);
-              o[0] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-              o[1] = make_uint4(lo[4], lo[5], lo[6], lo[7]);
-            }
-          }
+        for (int e = 0; e < 4; ++e) {
+          hi[e] = pack(v[2 * e], v[2 * e + 1]);
+          const float h0 = __uint_as_float(hi[e] << 16), h1 = __uint_as_float(hi[e] & 0xffff0000u);
+          // an infinite value is all in hi
+          lo[e] = pack(fabsf(h0) <= 3.402823466e38f ? v[2 * e] - h0 : 0.f,
+                       fabsf(h1) <= 3.402823466e38f ? v[2 * e + 1] - h1 : 0.f);
+        }
+        if (live) {
+          uint16_t* o = p.out + pr * 2 * p.half + c;
+          *reinterpret_cast<uint4*>(o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4*>(o + p.half) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
+      }
+    } else {
+      for (int c = 8 * group; c < p.R; c += 8 * nc) {
+        float v[8], w[8];
+        load8(c, v);
+        load8(p.half + c, w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] += w[e];
+        if (!live) continue;
+        if (p.mode == GRAD_ROWS) {
+          *reinterpret_cast<uint4*>(p.out + pr * p.R + c) =
+              make_uint4(pack(v[0], v[1]), pack(v[2], v[3]), pack(v[4], v[5]), pack(v[6], v[7]));
         } else {
-          for (int c = 0; c < p.R; c += 16) {
-            float v[16], w[16];
-            load16(c, v);
-            load16(p.half + c, w);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) v[e] += w[e];
-            if (!live) continue;
-            if (p.mode == GRAD_ROWS) {
-#pragma unroll
-              for (int h = 0; h < 2; ++h)
-                if (c + 8 * h < p.R)
-                  *reinterpret_cast<uint4*>(p.out + pr * p.R + c + 8 * h) =
-                      make_uint4(pack(v[8 * h], v[8 * h + 1]), pack(v[8 * h + 2], v[8 * h + 3]),
-                                 pack(v[8 * h + 4], v[8 * h + 5]), pack(v[8 * h + 6], v[8 * h + 7]));
-            } else {
-#pragma unroll
-              for (int e = 0; e < 16; ++e)
-                if (c + e < p.R)
-                  reinterpret_cast<__nv_bfloat16*>(p.out)[static_cast<size_t>(c + e) * p.ldo + pr] =
-                      __float2bfloat16_rn(v[e]);
-            }
-          }
+          for (int e = 0; e < 8; ++e)
+            reinterpret_cast<__nv_bfloat16*>(p.out)[static_cast<size_t>(c + e) * p.ldo + pr] =
+                __float2bfloat16_rn(v[e]);
         }
       }
     }
   }
-  tc_fence_before();
   __syncthreads();
+  cluster_sync_all();  // no CTA leaves while another may still read its sums
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, BN);
@@ -351,6 +348,7 @@ __global__ void __launch_bounds__(kGradThreads)
 // next one.  Persistent; the tiles of a last, partial round are split along N.
 constexpr int kDxStages = 6;
 constexpr int kDxStage = 32768;
+constexpr int kDxMaxParts = 4;
 
 struct GradDxParams {
   uint16_t* dX;
@@ -581,14 +579,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
           last = atomicAdd(p.count + (w.st * 2 + rank) * 4 + q, 1u) == static_cast<uint32_t>(w.parts - 1);
         if (__shfl_sync(0xffffffffu, last, 0)) {
           __threadfence();
+          // an L2 round trip per 16 columns: every part's loads go out before the first sum
           for (int c = 0; c < kn; c += 16) {
-            float v[16];
+            float v[16], x[kDxMaxParts][16];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) v[e] = 0.f;
-            for (int k = 0; k < w.parts; ++k) {
-              const float* src = parts + k * kPartStride + c * 128;
+            for (int k = 0; k < kDxMaxParts; ++k)
 #pragma unroll
-              for (int e = 0; e < 16; ++e) v[e] += __ldcg(src + e * 128);
+              for (int e = 0; e < 16; ++e)
+                x[k][e] = k < w.parts ? __ldcg(parts + k * kPartStride + (c + e) * 128) : 0.f;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              v[e] = x[0][e];
+#pragma unroll
+              for (int k = 1; k < kDxMaxParts; ++k) v[e] += x[k][e];
             }
             store16(c, v);
           }
