@@ -1427,10 +1427,10 @@ int salr_load(const void* buf, int64_t buf_bytes, void* stream, salr_handle* out
 namespace {
 
 // CTAs that share a row tile's reduction (a cluster): the largest power of two up to 8 that
-// leaves all CTAs resident at once.
-int grad_cluster(int tiles, int slots) {
+// leaves all CTAs resident at once and each of them at least two chunks.
+int grad_cluster(int tiles, int chunks, int slots) {
   int c = 1;
-  while (c < 8 && tiles * c * 2 <= slots) c *= 2;
+  while (c < 8 && tiles * c * 2 <= slots && chunks >= 4 * c) c *= 2;
   return c;
 }
 
@@ -1454,7 +1454,7 @@ TileSplit dx_split(int tiles, int kb, int pairs) {
 }
 
 template <int BN>
-int launch_grad_skinny(const GradSkinnyParams& p, const CUtensorMap* m, cudaStream_t st) {
+int launch_grad_skinny(const GradSkinnyParams& p, const CUtensorMap* m, bool overlap, cudaStream_t st) {
   static std::atomic<bool> attr_set[64];  // zero-initialised: false
   int dev = 0;
   SALR_TRY(cudaGetDevice(&dev));
@@ -1465,18 +1465,21 @@ int launch_grad_skinny(const GradSkinnyParams& p, const CUtensorMap* m, cudaStre
     attr_set[dev] = true;
   }
   const int tiles = p.p[0].tiles + p.p[1].tiles;
-  const int nc = grad_cluster(tiles, (BN == 256 ? 1 : 2) * device_sms(dev));
+  const int chunks = std::max(p.p[0].tiles ? p.p[0].chunks : 0, p.p[1].tiles ? p.p[1].chunks : 0);
+  const int nc = grad_cluster(tiles, chunks, (BN == 256 ? 1 : 2) * device_sms(dev));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(tiles * nc));
   cfg.blockDim = dim3(kGradThreads);
   cfg.dynamicSmemBytes = GradSkinny<BN>::kSmemBytes;
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = static_cast<unsigned>(nc);
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = overlap ? 2 : 1;
   SALR_TRY(cudaLaunchKernelEx(&cfg, grad_skinny_kernel<BN>, p, nc, m[0], m[1], m[2], m[3]));
   return SALR_OK;
 }
@@ -1490,8 +1493,17 @@ int launch_grad_dx(const GradDxParams& p, const CUtensorMap* m, int pairs, cudaS
     SALR_TRY(cudaFuncSetAttribute(grad_dx_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kDxSmemBytes));
     attr_set[dev] = true;
   }
-  grad_dx_kernel<<<2 * pairs, kGradThreads, kDxSmemBytes, st>>>(p, m[0], m[1], m[2], m[3]);
-  SALR_TRY(cudaGetLastError());
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs));
+  cfg.blockDim = dim3(kGradThreads);
+  cfg.dynamicSmemBytes = kDxSmemBytes;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  SALR_TRY(cudaLaunchKernelEx(&cfg, grad_dx_kernel, p, m[0], m[1], m[2], m[3]));
   return SALR_OK;
 }
 
@@ -1594,16 +1606,19 @@ int salr_linear_backward(const void* dY, const void* X, int64_t M64, salr_handle
     CUtensorMap m[4];
     std::memset(m, 0, sizeof(m));
     int rc = SALR_OK;
+    // The expansion first: the kernels after it overlap the ends of their predecessors, and
+    // dX waits for the u kernel, which ends after the expansion.
+    if (dX) SALR_TRY(launch_expand(h, W, st));
     if (pt.tiles + pu.tiles > 0) {
       if (pt.tiles && (!make_map(&m[0], X, K, M, 64, 128) || !make_map(&m[1], A_cat, R, K, 64, 64)))
         return SALR_ERR_CUDA;
       if (pu.tiles && (!make_map(&m[2], dY, N, M, 64, 128) || !make_map(&m[3], B_cat, N, R, 64, half)))
         return SALR_ERR_CUDA;
-      rc = half == 64 ? launch_grad_skinny<64>(s1, m, st) : launch_grad_skinny<128>(s1, m, st);
+      rc = half == 64 ? launch_grad_skinny<64>(s1, m, dX != nullptr, st)
+                      : launch_grad_skinny<128>(s1, m, dX != nullptr, st);
       if (rc != SALR_OK) return rc;
     }
     if (dX) {
-      SALR_TRY(launch_expand(h, W, st));
       if (!make_map(&m[0], dY, N, M, 64, 128) || !make_map(&m[1], W, K, N, 64, 64)) return SALR_ERR_CUDA;
       if (R > 0 && (!make_map(&m[2], u, 2 * half, M, 64, 128) || !make_map(&m[3], A_cat, R, K, 64, 128)))
         return SALR_ERR_CUDA;
@@ -1615,7 +1630,9 @@ int salr_linear_backward(const void* dY, const void* X, int64_t M64, salr_handle
         return SALR_ERR_CUDA;
       if (pb.tiles && (!make_map(&m[2], dY, N, M, 64, 64) || !make_map(&m[3], t, 2 * half, M, 64, 64)))
         return SALR_ERR_CUDA;
-      rc = half == 64 ? launch_grad_skinny<128>(s2, m, st) : launch_grad_skinny<256>(s2, m, st);
+      // dX lets it start only once u and t are complete; without dX it waits in stream order
+      rc = half == 64 ? launch_grad_skinny<128>(s2, m, dX != nullptr, st)
+                      : launch_grad_skinny<256>(s2, m, dX != nullptr, st);
     }
     return rc;
   };

@@ -8,6 +8,9 @@
 // whose reduction index is its row index is read MN-major (transposed by the tensor core),
 // so nothing is transposed in memory.
 //
+// The launches overlap at their ends (programmatic dependent launch): each kernel starts as
+// the SMs of the one before it fall free, and waits for it where it reads its results.
+//
 // 1. grad_skinny_kernel, t and u in one launch (two problems): 128 tokens x all ranks per
 //    CTA, the reduction over K or N split over CTAs.  The fp32 result is stored as two bf16
 //    parts side by side, hi = bf16(t) and lo = bf16(t - hi), so that the next products take
@@ -134,18 +137,20 @@ struct GradSkinny {
   // two CTAs an SM up to 128 columns, one with 256
   static constexpr int kStages = BN == 128 ? 3 : 4;
   static constexpr int kSmemBytes = kStages * kStage + 1024 + 256;
-  static_assert(kStages * kStage >= BN * 512, "the stages hold the fp32 sums at the end");
+  static_assert(kStages * kStage >= (BN + 4) * 512, "the stages hold the fp32 sums at the end");
 };
 
-// One float of shared memory of a CTA of the cluster.
-__device__ __forceinline__ float ld_cluster(uint32_t cluster_addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr));
+// 16 bytes of shared memory of a CTA of the cluster.
+__device__ __forceinline__ float4 ld_cluster4(uint32_t cluster_addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(cluster_addr));
   return v;
 }
 
 // A cluster of `nc` CTAs (1 to 8) takes a row tile, each CTA a part of its reduction.  The
-// parts' fp32 sums then lie in the CTAs' shared memory ([column][row], where the stages
+// parts' fp32 sums then lie in the CTAs' shared memory ([row][column], where the stages
 // were), and each CTA adds up and writes 128 / nc of the rows, in the order of the parts.
 // Parts that met in L2 instead, added up by the last one to arrive, spent most of the time
 // in that one CTA's chain of L2 reads: up_proj M = 2048 took 60 + 65 us for the two
@@ -169,6 +174,7 @@ __global__ void __launch_bounds__(kGradThreads)
   const int c0 = static_cast<int>(static_cast<long long>(part) * p.chunks / nc);
   const int c1 = static_cast<int>(static_cast<long long>(part + 1) * p.chunks / nc);
   const int p0 = tile * 128;
+  griddep_launch_dependents();
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < L::kStages; ++s) {
@@ -252,85 +258,90 @@ __global__ void __launch_bounds__(kGradThreads)
   }
   __syncthreads();  // every product is in TMEM, and the stages are free
   const bool ok = *abort_flag == 0;
-  float* sums = reinterpret_cast<float*>(smem);  // [BN][128]
+  // [128 rows][BN + 4 columns]: with the pad, a quarter-warp's 16-byte accesses fall on
+  // different banks both along a row and down a column
+  float* sums = reinterpret_cast<float*>(smem);
+  constexpr int kRow = BN + 4;
   if (warp >= 2 && ok) {
     const int q = warp & 3;  // TMEM lane quarter
     const uint32_t tm = tmem + (static_cast<uint32_t>(32 * q) << 16);
+    float* dst = sums + (32 * q + lane) * kRow;
     tc_fence_after();
     for (int c = 0; c < BN; c += 16) {
       uint32_t v[16];
       tmem_ld16(tm + c, v);
       tmem_ld_wait();
 #pragma unroll
-      for (int e = 0; e < 16; ++e)  // an empty part adds nothing
-        sums[(c + e) * 128 + 32 * q + lane] = c1 > c0 ? __uint_as_float(v[e]) : 0.f;
+      for (int e = 0; e < 16; e += 4)  // an empty part adds nothing
+        *reinterpret_cast<uint4*>(dst + c + e) =
+            c1 > c0 ? make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]) : make_uint4(0, 0, 0, 0);
     }
     tc_fence_before();
   }
   __syncthreads();
   cluster_sync_all();
   if (warp >= 2 && ok) {
-    const int rows = 128 / nc, tid = threadIdx.x - 64;
-    const int row = part * rows + tid % rows, group = tid / rows;  // nc groups of columns
-    const uint32_t base = smem_u32(sums + row);
+    const int rows = 128 / nc, r0 = part * rows, tid = threadIdx.x - 64;
     uint32_t from[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) from[k] = map_to_rank(base, k < nc ? k : 0);
-    auto load8 = [&](int c, float (&v)[8]) {
+    for (int k = 0; k < 8; ++k) from[k] = map_to_rank(smem_u32(sums), k < nc ? k : 0);
+    // four columns of a row, summed over the parts in order
+    auto load4 = [&](int row, int c) {
+      const uint32_t at = static_cast<uint32_t>(row * kRow + c) * 4;
+      float4 x[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = 0.f;
+      for (int k = 0; k < 8; ++k) x[k] = k < nc ? ld_cluster4(from[k] + at) : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (k < nc) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] += ld_cluster(from[k] + (c + e) * 512);
-        }
+      for (int k = 1; k < 8; ++k) x[0].x += x[k].x, x[0].y += x[k].y, x[0].z += x[k].z, x[0].w += x[k].w;
+      return x[0];
     };
     auto pack = [](float a, float b) {
       const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
       return *reinterpret_cast<const uint32_t*>(&h);
     };
-    const size_t pr = static_cast<size_t>(p0) + row;
-    const bool live = p0 + row < p.P;
-    if (p.mode == GRAD_SPLIT) {
-      for (int c = 8 * group; c < BN; c += 8 * nc) {
-        float v[8];
-        load8(c, v);
-        uint32_t hi[4], lo[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          hi[e] = pack(v[2 * e], v[2 * e + 1]);
-          const float h0 = __uint_as_float(hi[e] << 16), h1 = __uint_as_float(hi[e] & 0xffff0000u);
-          // an infinite value is all in hi
-          lo[e] = pack(fabsf(h0) <= 3.402823466e38f ? v[2 * e] - h0 : 0.f,
-                       fabsf(h1) <= 3.402823466e38f ? v[2 * e + 1] - h1 : 0.f);
-        }
-        if (live) {
-          uint16_t* o = p.out + pr * 2 * p.half + c;
-          *reinterpret_cast<uint4*>(o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4*>(o + p.half) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    // what a bf16 pair leaves of a and b (nothing of an infinite value: it is all in hi)
+    auto rest = [&](uint32_t h, float a, float b) {
+      const float h0 = __uint_as_float(h << 16), h1 = __uint_as_float(h & 0xffff0000u);
+      return pack(fabsf(h0) <= 3.402823466e38f ? a - h0 : 0.f, fabsf(h1) <= 3.402823466e38f ? b - h1 : 0.f);
+    };
+    if (p.mode == GRAD_COLS) {  // lanes down the rows, which are neighbours in the output
+      for (int i = tid; i < rows * (p.R / 4); i += 128) {
+        const int row = r0 + i % rows, c = i / rows * 4;
+        float4 v = load4(row, c);
+        const float4 w = load4(row, p.half + c);
+        v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
+        if (p0 + row < p.P) {
+          __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(p.out) + static_cast<size_t>(c) * p.ldo + p0 + row;
+          o[0] = __float2bfloat16_rn(v.x);
+          o[static_cast<size_t>(p.ldo)] = __float2bfloat16_rn(v.y);
+          o[2 * static_cast<size_t>(p.ldo)] = __float2bfloat16_rn(v.z);
+          o[3 * static_cast<size_t>(p.ldo)] = __float2bfloat16_rn(v.w);
         }
       }
-    } else {
-      for (int c = 8 * group; c < p.R; c += 8 * nc) {
-        float v[8], w[8];
-        load8(c, v);
-        load8(p.half + c, w);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] += w[e];
-        if (!live) continue;
-        if (p.mode == GRAD_ROWS) {
-          *reinterpret_cast<uint4*>(p.out + pr * p.R + c) =
-              make_uint4(pack(v[0], v[1]), pack(v[2], v[3]), pack(v[4], v[5]), pack(v[6], v[7]));
+    } else {  // lanes along the columns
+      const int quads = (p.mode == GRAD_SPLIT ? BN : p.R) / 4;
+      for (int i = tid; i < rows * quads; i += 128) {
+        const int row = r0 + i / quads, c = i % quads * 4;
+        const bool live = p0 + row < p.P;
+        const size_t pr = static_cast<size_t>(p0) + row;
+        float4 v = load4(row, c);
+        if (p.mode == GRAD_SPLIT) {
+          const uint32_t h0 = pack(v.x, v.y), h1 = pack(v.z, v.w);
+          if (live) {
+            uint16_t* o = p.out + pr * 2 * p.half + c;
+            *reinterpret_cast<uint2*>(o) = make_uint2(h0, h1);
+            *reinterpret_cast<uint2*>(o + p.half) = make_uint2(rest(h0, v.x, v.y), rest(h1, v.z, v.w));
+          }
         } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            reinterpret_cast<__nv_bfloat16*>(p.out)[static_cast<size_t>(c + e) * p.ldo + pr] =
-                __float2bfloat16_rn(v[e]);
+          const float4 w = load4(row, p.half + c);
+          v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
+          if (live) *reinterpret_cast<uint2*>(p.out + pr * p.R + c) = make_uint2(pack(v.x, v.y), pack(v.z, v.w));
         }
       }
     }
   }
+  // this grid ends after the one before it, whether or not it used its results
+  if (threadIdx.x == 0) griddep_wait();
   __syncthreads();
   cluster_sync_all();  // no CTA leaves while another may still read its sums
   if (warp == 1) {
@@ -438,6 +449,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
       int s = 0, ph = 0;
       long long issued = 0;
       bool ok = true;
+      // u, and the dense weight: the u kernel ends after the expansion
+      griddep_wait();
+      griddep_launch_dependents();
       for (int u = pair; u < p.units && ok; u += pairs) {
         const GradDxUnit w = grad_dx_unit(p, u);
         const int row = w.m * 256 + static_cast<int>(rank) * 128;

@@ -600,6 +600,7 @@ __global__ void __launch_bounds__(128) expand_dense_kernel(const uint8_t* __rest
                                                            int K, int nblocks,
                                                            uint16_t* __restrict__ out,
                                                            int* status) {
+  griddep_launch_dependents();  // a kernel launched to overlap this one waits for it itself
   extern __shared__ uint4 exp_smem[];
   uint8_t* const cb0 = reinterpret_cast<uint8_t*>(exp_smem);  // two staging buffers
   auto cb = [&](int buf) { return cb0 + buf * kExpandBuf; };

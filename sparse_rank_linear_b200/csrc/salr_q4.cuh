@@ -251,6 +251,7 @@ __global__ void __launch_bounds__(32 * kQ4Warps)
 template <int GROUP, bool ZEROS>
 __global__ void __launch_bounds__(256) q4_expand_kernel(const Q4View w, uint16_t* __restrict__ out) {
   constexpr int NG = kQ4Unit / GROUP;
+  griddep_launch_dependents();  // a kernel launched to overlap this one waits for it itself
   const int lane = threadIdx.x & 31, g = lane >> 2, tl = lane & 3;
   const long long total = static_cast<long long>(w.N / 16) * w.units;
   const long long step = static_cast<long long>(gridDim.x) * (blockDim.x >> 5);
