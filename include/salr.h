@@ -362,7 +362,7 @@ SALR_API int salr_residual_adapter(const void* W, salr_handle h, int64_t r, cons
  *
  * salr_linear on such a handle: for M <= 64 the codes are rebuilt in registers (q - z
  * exactly, in bf16), products and sums are fp32, each group's sum is scaled in fp32, t =
- * X A_cat stays fp32, and results repeat bit for bit.  Two kernels with adapters, one
+ * X A_cat is kept as two bf16 parts (16 bits of significand), and results repeat bit for bit.  Two kernels with adapters, one
  * without.  Above that, the weight is expanded to a dense bf16 scratch (s (q - z) rounded
  * once) and the rest is as described under salr_linear.  The handle must be on the current
  * device (else SALR_ERR_INVALID); its t buffer (M <= 64) is not safe to share between calls

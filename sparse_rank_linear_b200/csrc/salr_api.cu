@@ -96,7 +96,7 @@ struct salr_weight_s {
   size_t y_cap;
   int group;     // 4-bit weights: columns per scale; 0: bitmap weight
   Q4View q4;     // 4-bit weights: the packed codes, scales and zero points, in mem
-  float* q4_t;   // 4-bit weights: t = X A_cat of the small-M kernel, 64 x 128 fp32, in mem
+  uint16_t* q4_t;  // 4-bit weights: t = X A_cat of the small-M kernel, 64 x 256 bf16, in mem
 };
 
 namespace {
@@ -300,8 +300,8 @@ int ensure_tscratch(salr_weight_s* h, int64_t M, cudaStream_t st) {
 
 template <int GROUP>
 cudaError_t launch_q4_expand(const salr_weight_s* h, uint16_t* out, cudaStream_t st) {
-  const long long units = h->N / 16 * h->q4.units;
-  const unsigned g = static_cast<unsigned>(std::min<long long>((units + 7) / 8, 8ll * device_sms(h->device)));
+  const long long tiles = h->N / 128 * (h->K / 64);
+  const unsigned g = static_cast<unsigned>(std::min<long long>(tiles, 32ll * device_sms(h->device)));
   if (h->q4.zeros)
     q4_expand_kernel<GROUP, true><<<g, 256, 0, st>>>(h->q4, out);
   else
@@ -714,52 +714,117 @@ int check_linear_args(const void* X, int64_t M, salr_handle h, const void* A, co
   return SALR_OK;
 }
 
-template <int NT, int GROUP>
-int launch_q4(const salr_weight_s* h, const uint16_t* X, int M, const float* t, const uint16_t* B,
-              int R, uint16_t* Y, cudaStream_t st) {
+// CTAs that share a row block's columns (a cluster), for `stages` stages of 128 columns: the
+// count that keeps the busiest SM least busy, each CTA costing about kQ4CtaCost stages beside
+// its own.
+constexpr int kQ4CtaCost = 3;
+int q4_parts(int blocks, int stages, int sms) {
+  int best = 1;
+  long long cost = -1;
+  for (int p = 1; p <= 8 && p <= stages; p *= 2) {
+    const long long c = static_cast<long long>((blocks * p + sms - 1) / sms) * ((stages + p - 1) / p + kQ4CtaCost);
+    if (cost < 0 || c < cost) {
+      cost = c;
+      best = p;
+    }
+  }
+  return best;
+}
+
+template <int NT, int GROUP, bool ZEROS>
+int launch_q4_kernel(const Q4Params& p, const CUtensorMap* m, int dev, cudaStream_t st) {
+  using L = Q4Layout<NT>;
+  const auto kern = q4_linear_kernel<NT, GROUP, ZEROS>;
+  static std::atomic<bool> attr_set[64];  // zero-initialised: false
+  if (!attr_set[dev]) {
+    SALR_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmemBytes));
+    attr_set[dev] = true;
+  }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(h->N / 16));
-  cfg.blockDim = dim3(32 * kQ4Warps);
+  cfg.gridDim = dim3(static_cast<unsigned>(p.w.N / 128 * p.parts));
+  cfg.blockDim = dim3(L::kThreads);
+  cfg.dynamicSmemBytes = L::kSmemBytes;
   cfg.stream = st;
-  // Directly after the t kernel, the launch may overlap it: codes, X and B were complete
+  // Directly after the t kernel, the launch may overlap it: records, X and B were complete
   // before that kernel started, and t is waited for.
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(p.parts);
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = R > 0 ? 1 : 0;
-  if (h->q4.zeros)
-    SALR_TRY(cudaLaunchKernelEx(&cfg, q4_linear_kernel<NT, GROUP, true>, h->q4, X, M, t, B, R, Y));
-  else
-    SALR_TRY(cudaLaunchKernelEx(&cfg, q4_linear_kernel<NT, GROUP, false>, h->q4, X, M, t, B, R, Y));
+  cfg.numAttrs = p.R > 0 ? 2 : 1;
+  SALR_TRY(cudaLaunchKernelEx(&cfg, kern, p, m[0], m[1], m[2]));
+  return SALR_OK;
+}
+
+template <int NT>
+int launch_q4(const Q4Params& p, const CUtensorMap* m, int dev, cudaStream_t st) {
+  const int g = p.w.group;
+  if (p.w.zeros)
+    return g == 32   ? launch_q4_kernel<NT, 32, true>(p, m, dev, st)
+           : g == 64 ? launch_q4_kernel<NT, 64, true>(p, m, dev, st)
+                     : launch_q4_kernel<NT, 128, true>(p, m, dev, st);
+  return g == 32   ? launch_q4_kernel<NT, 32, false>(p, m, dev, st)
+         : g == 64 ? launch_q4_kernel<NT, 64, false>(p, m, dev, st)
+                   : launch_q4_kernel<NT, 128, false>(p, m, dev, st);
+}
+
+template <int MT>
+int launch_q4_t(const uint16_t* X, const uint16_t* A, int M, int K, int R, uint16_t* t, cudaStream_t st) {
+  // every thread of a part gets two rows of A or more
+  int parts = 1;
+  while (parts < 8 && K / (2 * parts) >= 2 * kQ4TThreads) parts *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((R + 31) / 32 * 4 * parts), static_cast<unsigned>((M + MT - 1) / MT));
+  cfg.blockDim = dim3(kQ4TThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(parts);
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  SALR_TRY(cudaLaunchKernelEx(&cfg, q4_t_kernel<MT>, X, A, M, K, R, parts, t));
   return SALR_OK;
 }
 
 // The layer on a 4-bit weight for up to 64 tokens: a t kernel (with adapters) and the
 // layer kernel, which starts while t is being computed.
-int launch_q4_linear(const void* Xv, int64_t M64, salr_handle h, const void* A, const void* Bv,
-                     int64_t R64, void* Yv, cudaStream_t st) {
+int launch_q4_linear(const void* X, int64_t M64, salr_handle h, const void* A, const void* B,
+                     int64_t R64, void* Y, cudaStream_t st) {
   const int M = static_cast<int>(M64), R = static_cast<int>(R64), K = static_cast<int>(h->K);
-  const uint16_t* X = static_cast<const uint16_t*>(Xv);
-  const uint16_t* B = static_cast<const uint16_t*>(Bv);
-  uint16_t* Y = static_cast<uint16_t*>(Yv);
+  const int nt = M <= 8 ? 1 : M <= 16 ? 2 : M <= 32 ? 4 : M <= 48 ? 6 : 8;
+  SALR_TRY(apply_wait_limit(st));
+  CUtensorMap m[3];
+  std::memset(m, 0, sizeof(m));
+  if (!make_map(&m[0], X, K, M, 64, 8 * nt)) return SALR_ERR_CUDA;
   if (R > 0) {
-    const uint16_t* Ab = static_cast<const uint16_t*>(A);
-    if (M == 1)
-      q4_t_kernel<1><<<dim3(R / 8, 1), kQ4TThreads, 0, st>>>(X, Ab, M, K, R, h->q4_t);
-    else
-      q4_t_kernel<8><<<dim3(R / 8, (M + 7) / 8), kQ4TThreads, 0, st>>>(X, Ab, M, K, R, h->q4_t);
-    SALR_TRY(cudaGetLastError());
+    if (!make_map(&m[1], h->q4_t, 256, kQ4MaxTokens, 64, 8 * nt)) return SALR_ERR_CUDA;
+    if (!make_map(&m[2], B, h->N, R, 64, 32)) return SALR_ERR_CUDA;
+    const uint16_t *Xb = static_cast<const uint16_t*>(X), *Ab = static_cast<const uint16_t*>(A);
+    const int rc = M == 1 ? launch_q4_t<1>(Xb, Ab, M, K, R, h->q4_t, st)
+                          : launch_q4_t<8>(Xb, Ab, M, K, R, h->q4_t, st);
+    if (rc != SALR_OK) return rc;
   }
-#define SALR_Q4_TOKENS(NT)                                                     \
-  return h->group == 32   ? launch_q4<NT, 32>(h, X, M, h->q4_t, B, R, Y, st)   \
-         : h->group == 64 ? launch_q4<NT, 64>(h, X, M, h->q4_t, B, R, Y, st)   \
-                          : launch_q4<NT, 128>(h, X, M, h->q4_t, B, R, Y, st)
-  if (M <= 8) SALR_Q4_TOKENS(1);
-  if (M <= 16) SALR_Q4_TOKENS(2);
-  if (M <= 32) SALR_Q4_TOKENS(4);
-  SALR_Q4_TOKENS(8);
-#undef SALR_Q4_TOKENS
+  Q4Params p{};
+  p.w = h->q4;
+  p.Y = static_cast<uint16_t*>(Y);
+  p.status = h->status;
+  p.M = M;
+  p.R = R;
+  const int sms = device_sms(h->device);
+  p.parts = q4_parts(static_cast<int>(h->N / 128), (K + kQ4Cols - 1) / kQ4Cols, sms);
+  const int dev = h->device;
+  if (dev < 0 || dev >= 64) return SALR_ERR_UNSUPPORTED;
+  switch (nt) {
+    case 1: return launch_q4<1>(p, m, dev, st);
+    case 2: return launch_q4<2>(p, m, dev, st);
+    case 4: return launch_q4<4>(p, m, dev, st);
+    case 6: return launch_q4<6>(p, m, dev, st);
+    default: return launch_q4<8>(p, m, dev, st);
+  }
 }
 
 }  // namespace
@@ -953,11 +1018,11 @@ int q4_make(const void* codes, const void* scales, const void* zeros, int64_t N,
   h->keep = K;
   h->nnz = N * K;
   h->group = static_cast<int>(group);
-  const int units = static_cast<int>((K + kQ4Unit - 1) / kQ4Unit);
-  const int64_t all = N / 16 * units;
-  const int64_t pairs = all * 8 * (kQ4Unit / group);
-  const size_t cb = round256(all * kQ4UnitBytes), sb = round256(pairs * 4);
-  const size_t zb = zeros ? round256(pairs * 2) : 0;
+  h->q4.N = static_cast<int>(N);
+  h->q4.K = static_cast<int>(K);
+  h->q4.group = h->group;
+  h->q4.zeros = zeros ? 1 : 0;
+  h->blob_bytes = N / 128 * h->q4.block_bytes();
   auto fail = [&](int code) {
     if (scratch) cudaFreeAsync(scratch, st);
     cudaStreamSynchronize(st);
@@ -965,24 +1030,18 @@ int q4_make(const void* codes, const void* scales, const void* zeros, int64_t N,
     return code;
   };
   cudaError_t e;
-  const size_t tb = kQ4MaxTokens * 128 * sizeof(float);
-  if ((e = alloc_handle_memory(h, cb + sb + zb + tb, st)) != cudaSuccess) return fail(cuda_status(e));
-  h->q4.codes = h->blob;
-  h->q4.scales = reinterpret_cast<const uint32_t*>(h->blob + cb);
-  h->q4.zeros = zeros ? reinterpret_cast<const uint16_t*>(h->blob + cb + sb) : nullptr;
-  h->q4_t = reinterpret_cast<float*>(h->blob + cb + sb + zb);
-  h->q4.N = static_cast<int>(N);
-  h->q4.K = static_cast<int>(K);
-  h->q4.units = units;
-  h->blob_bytes = all * kQ4UnitBytes + pairs * (zeros ? 6 : 4);
-  if ((e = cudaMemsetAsync(h->status, 0, sizeof(int), st)) != cudaSuccess) return fail(cuda_status(e));
-  const long long words = all * (kQ4UnitBytes / 4);
+  const size_t data = round256(h->blob_bytes), tb = kQ4MaxTokens * 256 * sizeof(uint16_t);
+  if ((e = alloc_handle_memory(h, data + tb, st)) != cudaSuccess) return fail(cuda_status(e));
+  h->q4.data = h->blob;
+  h->q4_t = reinterpret_cast<uint16_t*>(h->blob + data);
+  // t rows of tokens that no call has had yet are read (and their products dropped)
+  if ((e = cudaMemsetAsync(h->status, 0, sizeof(int), st)) != cudaSuccess ||
+      (e = cudaMemsetAsync(h->q4_t, 0, tb, st)) != cudaSuccess)
+    return fail(cuda_status(e));
+  const long long words = N / 128 * (K / 64) * 1024;
   const unsigned grid = static_cast<unsigned>(std::min<long long>((words + 255) / 256, 16ll * device_sms(h->device)));
-  q4_pack_kernel<<<grid, 256, 0, st>>>(
-      static_cast<const uint32_t*>(codes), static_cast<const uint16_t*>(scales),
-      static_cast<const uint8_t*>(zeros), h->q4.N, h->q4.K, h->group, units,
-      reinterpret_cast<uint32_t*>(h->blob), reinterpret_cast<uint32_t*>(h->blob + cb),
-      reinterpret_cast<uint16_t*>(h->blob + cb + sb), h->status);
+  q4_pack_kernel<<<grid, 256, 0, st>>>(static_cast<const uint32_t*>(codes), static_cast<const uint16_t*>(scales),
+                                       static_cast<const uint8_t*>(zeros), h->q4, h->status);
   if ((e = cudaGetLastError()) != cudaSuccess) return fail(cuda_status(e));
   int status[2] = {0, 0};
   if ((e = cudaMemcpyAsync(status, h->status, sizeof(int), cudaMemcpyDeviceToHost, st)) != cudaSuccess ||
@@ -1030,7 +1089,7 @@ int salr_q4_encode(const void* W, int64_t N, int64_t K, int64_t group, int symme
   int* flags = reinterpret_cast<int*>(mem);
   cudaError_t e = cudaMemsetAsync(flags, 0, sizeof(int), st);
   if (e == cudaSuccess) {
-    const long long warps = static_cast<long long>(N) * ((K + kQ4Unit - 1) / kQ4Unit);
+    const long long warps = static_cast<long long>(N) * ((K + 255) / 256);
     const unsigned grid = static_cast<unsigned>(std::min<long long>((warps + 7) / 8, 8ll * device_sms(dev)));
     q4_quantise_kernel<<<grid, 256, 0, st>>>(
         static_cast<const uint16_t*>(W), static_cast<int>(N), static_cast<int>(K), static_cast<int>(group),

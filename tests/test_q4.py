@@ -104,10 +104,8 @@ def test_pack_and_decode(N, K, group, zeros):
     codes, s, z, W, _ = make(N, K, group, zeros)
     w = salr.pack_q4(codes, s, z)
     assert torch.equal(w.decode(), W.bfloat16())  # s (q - z) is exact in fp32, rounded once
-    units = -(-K // 256)
-    pairs = N // 16 * units * 8 * (256 // group)
     assert w.info() == {"N": N, "K": K, "nnz": N * K,
-                        "bytes": N // 16 * units * 2048 + pairs * (6 if zeros else 4)}
+                        "bytes": N * K // 2 + N * K // group * (3 if zeros else 2)}
     w.free()
 
 
