@@ -365,8 +365,9 @@ SALR_API int salr_residual_adapter(const void* W, salr_handle h, int64_t r, cons
  * X A_cat is kept as two bf16 parts (16 bits of significand), and results repeat bit for bit.  Two kernels with adapters, one
  * without.  Above that, the weight is expanded to a dense bf16 scratch (s (q - z) rounded
  * once) and the rest is as described under salr_linear.  The handle must be on the current
- * device (else SALR_ERR_INVALID); its t buffer (M <= 64) is not safe to share between calls
- * that run concurrently on different streams, captured graphs among them.
+ * device (else SALR_ERR_INVALID); its arrival counts (M <= 64) are not safe to share between
+ * calls that run concurrently on different streams, captured graphs among them.  Scratch
+ * (t and partial sums) is the call's own, from the library's pool.
  */
 SALR_API int salr_q4_pack(const void* codes, const void* scales, const void* zeros, int64_t N,
                           int64_t K, int64_t group, void* stream, salr_handle* out);

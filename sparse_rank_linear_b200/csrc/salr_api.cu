@@ -96,7 +96,7 @@ struct salr_weight_s {
   size_t y_cap;
   int group;     // 4-bit weights: columns per scale; 0: bitmap weight
   Q4View q4;     // 4-bit weights: the packed codes, scales and zero points, in mem
-  uint16_t* q4_t;  // 4-bit weights: t = X A_cat of the small-M kernel, 64 x 256 bf16, in mem
+  uint32_t* q4_count;  // 4-bit weights: the small-M kernel's arrival counts, 8 a row block, in mem
 };
 
 namespace {
@@ -714,25 +714,12 @@ int check_linear_args(const void* X, int64_t M, salr_handle h, const void* A, co
   return SALR_OK;
 }
 
-// CTAs that share a row block's columns (a cluster), for `stages` stages of 128 columns: the
-// count that keeps the busiest SM least busy, each CTA costing about kQ4CtaCost stages beside
-// its own.
-constexpr int kQ4CtaCost = 3;
-int q4_parts(int blocks, int stages, int sms) {
-  int best = 1;
-  long long cost = -1;
-  for (int p = 1; p <= 8 && p <= stages; p *= 2) {
-    const long long c = static_cast<long long>((blocks * p + sms - 1) / sms) * ((stages + p - 1) / p + kQ4CtaCost);
-    if (cost < 0 || c < cost) {
-      cost = c;
-      best = p;
-    }
-  }
-  return best;
-}
+// Fewest stages of a CTA's range (below, its set-up and the sums' meeting cost more than
+// the stages).
+constexpr int kQ4MinStages = 4;
 
 template <int NT, int GROUP, bool ZEROS>
-int launch_q4_kernel(const Q4Params& p, const CUtensorMap* m, int dev, cudaStream_t st) {
+int launch_q4_kernel(const Q4Params& p, const CUtensorMap* m, int ctas, int dev, cudaStream_t st) {
   using L = Q4Layout<NT>;
   const auto kern = q4_linear_kernel<NT, GROUP, ZEROS>;
   static std::atomic<bool> attr_set[64];  // zero-initialised: false
@@ -741,90 +728,107 @@ int launch_q4_kernel(const Q4Params& p, const CUtensorMap* m, int dev, cudaStrea
     attr_set[dev] = true;
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.w.N / 128 * p.parts));
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
   cfg.blockDim = dim3(L::kThreads);
   cfg.dynamicSmemBytes = L::kSmemBytes;
   cfg.stream = st;
   // Directly after the t kernel, the launch may overlap it: records, X and B were complete
   // before that kernel started, and t is waited for.
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(p.parts);
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = p.R > 0 ? 2 : 1;
+  cfg.numAttrs = p.R > 0 ? 1 : 0;
   SALR_TRY(cudaLaunchKernelEx(&cfg, kern, p, m[0], m[1], m[2]));
   return SALR_OK;
 }
 
 template <int NT>
-int launch_q4(const Q4Params& p, const CUtensorMap* m, int dev, cudaStream_t st) {
-  const int g = p.w.group;
-  if (p.w.zeros)
-    return g == 32   ? launch_q4_kernel<NT, 32, true>(p, m, dev, st)
-           : g == 64 ? launch_q4_kernel<NT, 64, true>(p, m, dev, st)
-                     : launch_q4_kernel<NT, 128, true>(p, m, dev, st);
-  return g == 32   ? launch_q4_kernel<NT, 32, false>(p, m, dev, st)
-         : g == 64 ? launch_q4_kernel<NT, 64, false>(p, m, dev, st)
-                   : launch_q4_kernel<NT, 128, false>(p, m, dev, st);
-}
-
-template <int MT>
-int launch_q4_t(const uint16_t* X, const uint16_t* A, int M, int K, int R, uint16_t* t, cudaStream_t st) {
-  // every thread of a part gets two rows of A or more
-  int parts = 1;
-  while (parts < 8 && K / (2 * parts) >= 2 * kQ4TThreads) parts *= 2;
+int launch_q4_t(const CUtensorMap& mx, const CUtensorMap& ma, int M, int K, int R, uint16_t* t, int* status,
+                int dev, cudaStream_t st) {
+  using L = Q4TLayout<NT>;
+  static std::atomic<bool> attr_set[64];  // zero-initialised: false
+  if (!attr_set[dev]) {
+    SALR_TRY(cudaFuncSetAttribute(q4_t_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmemBytes));
+    attr_set[dev] = true;
+  }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((R + 31) / 32 * 4 * parts), static_cast<unsigned>((M + MT - 1) / MT));
-  cfg.blockDim = dim3(kQ4TThreads);
+  cfg.gridDim = dim3(kQ4TParts);
+  cfg.blockDim = dim3(L::kThreads);
+  cfg.dynamicSmemBytes = L::kSmemBytes;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(parts);
+  attr[0].val.clusterDim.x = kQ4TParts;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  SALR_TRY(cudaLaunchKernelEx(&cfg, q4_t_kernel<MT>, X, A, M, K, R, parts, t));
+  SALR_TRY(cudaLaunchKernelEx(&cfg, q4_t_kernel<NT>, mx, ma, M, K, R, t, status));
   return SALR_OK;
 }
 
-// The layer on a 4-bit weight for up to 64 tokens: a t kernel (with adapters) and the
+// The layer on a 4-bit weight for up to 8 NT tokens: a t kernel (with adapters) and the
 // layer kernel, which starts while t is being computed.
-int launch_q4_linear(const void* X, int64_t M64, salr_handle h, const void* A, const void* B,
-                     int64_t R64, void* Y, cudaStream_t st) {
-  const int M = static_cast<int>(M64), R = static_cast<int>(R64), K = static_cast<int>(h->K);
-  const int nt = M <= 8 ? 1 : M <= 16 ? 2 : M <= 32 ? 4 : M <= 48 ? 6 : 8;
+template <int NT>
+int launch_q4(const void* X, int M, salr_handle h, const void* A, const void* B, int R, void* Y,
+              cudaStream_t st) {
+  const int K = static_cast<int>(h->K), dev = h->device, blocks = static_cast<int>(h->N / 128);
+  if (dev < 0 || dev >= 64) return SALR_ERR_UNSUPPORTED;
   SALR_TRY(apply_wait_limit(st));
-  CUtensorMap m[3];
-  std::memset(m, 0, sizeof(m));
-  if (!make_map(&m[0], X, K, M, 64, 8 * nt)) return SALR_ERR_CUDA;
-  if (R > 0) {
-    if (!make_map(&m[1], h->q4_t, 256, kQ4MaxTokens, 64, 8 * nt)) return SALR_ERR_CUDA;
-    if (!make_map(&m[2], B, h->N, R, 64, 32)) return SALR_ERR_CUDA;
-    const uint16_t *Xb = static_cast<const uint16_t*>(X), *Ab = static_cast<const uint16_t*>(A);
-    const int rc = M == 1 ? launch_q4_t<1>(Xb, Ab, M, K, R, h->q4_t, st)
-                          : launch_q4_t<8>(Xb, Ab, M, K, R, h->q4_t, st);
-    if (rc != SALR_OK) return rc;
-  }
   Q4Params p{};
   p.w = h->q4;
   p.Y = static_cast<uint16_t*>(Y);
+  p.count = h->q4_count;
   p.status = h->status;
   p.M = M;
   p.R = R;
-  const int sms = device_sms(h->device);
-  p.parts = q4_parts(static_cast<int>(h->N / 128), (K + kQ4Cols - 1) / kQ4Cols, sms);
-  const int dev = h->device;
-  if (dev < 0 || dev >= 64) return SALR_ERR_UNSUPPORTED;
-  switch (nt) {
-    case 1: return launch_q4<1>(p, m, dev, st);
-    case 2: return launch_q4<2>(p, m, dev, st);
-    case 4: return launch_q4<4>(p, m, dev, st);
-    case 6: return launch_q4<6>(p, m, dev, st);
-    default: return launch_q4<8>(p, m, dev, st);
-  }
+  p.stages = (K + kQ4Cols - 1) / kQ4Cols;
+  p.total = static_cast<long long>(blocks) * p.stages;
+  // every CTA resident at once, the t kernel's beside them
+  const long long slots = static_cast<long long>(Q4Layout<NT>::kPerSm) * device_sms(dev) - (R > 0 ? kQ4TParts : 0);
+  const int ctas = static_cast<int>(std::max<long long>(1, std::min(slots, p.total / kQ4MinStages)));
+  CUtensorMap m[3], ma;
+  std::memset(m, 0, sizeof(m));
+  if (!make_map(&m[0], X, K, M, 64, 8 * NT)) return SALR_ERR_CUDA;
+  // scratch: [t][partial sums], where there are any
+  const size_t tb = R > 0 ? kQ4MaxTokens * 256 * sizeof(uint16_t) : 0;
+  const bool shared = p.total % ctas != 0 || (p.total / ctas) % p.stages != 0;
+  const size_t pb = shared ? 2 * static_cast<size_t>(ctas) * M * 128 * sizeof(float) : 0;
+  uint8_t* mem = nullptr;
+  if (tb + pb) SALR_TRY(dev_alloc_async(reinterpret_cast<void**>(&mem), tb + pb, st, kPoolScratch));
+  p.part = reinterpret_cast<float*>(mem + tb);
+  auto run = [&]() -> int {
+    if (R > 0) {
+      // t rows past M are not written: their products belong to no token
+      uint16_t* t = reinterpret_cast<uint16_t*>(mem);
+      if (!make_map(&m[1], t, 256, M, 64, 8 * NT) || !make_map(&m[2], B, h->N, R, 64, 32) ||
+          !make_map(&ma, A, R, K, 64, 64))
+        return SALR_ERR_CUDA;
+      const int rc = launch_q4_t<NT>(m[0], ma, M, K, R, t, h->status, dev, st);
+      if (rc != SALR_OK) return rc;
+    }
+    const int g = h->group;
+    if (p.w.zeros)
+      return g == 32   ? launch_q4_kernel<NT, 32, true>(p, m, ctas, dev, st)
+             : g == 64 ? launch_q4_kernel<NT, 64, true>(p, m, ctas, dev, st)
+                       : launch_q4_kernel<NT, 128, true>(p, m, ctas, dev, st);
+    return g == 32   ? launch_q4_kernel<NT, 32, false>(p, m, ctas, dev, st)
+           : g == 64 ? launch_q4_kernel<NT, 64, false>(p, m, ctas, dev, st)
+                     : launch_q4_kernel<NT, 128, false>(p, m, ctas, dev, st);
+  };
+  const int rc = run();
+  const cudaError_t e = mem ? cudaFreeAsync(mem, st) : cudaSuccess;
+  return rc != SALR_OK ? rc : cuda_status(e);
+}
+
+int launch_q4_linear(const void* X, int64_t M64, salr_handle h, const void* A, const void* B,
+                     int64_t R64, void* Y, cudaStream_t st) {
+  const int M = static_cast<int>(M64), R = static_cast<int>(R64);
+  if (M <= 8) return launch_q4<1>(X, M, h, A, B, R, Y, st);
+  if (M <= 16) return launch_q4<2>(X, M, h, A, B, R, Y, st);
+  if (M <= 32) return launch_q4<4>(X, M, h, A, B, R, Y, st);
+  if (M <= 48) return launch_q4<6>(X, M, h, A, B, R, Y, st);
+  return launch_q4<8>(X, M, h, A, B, R, Y, st);
 }
 
 }  // namespace
@@ -990,6 +994,8 @@ int salr_encode(const void* W, int64_t N, int64_t K, float sparsity, void* strea
 
 namespace {
 
+size_t q4_count_bytes(const salr_weight_s* h) { return static_cast<size_t>(h->N / 128) * 8 * sizeof(uint32_t); }
+
 bool valid_group(int64_t K, int64_t group) {
   return (group == 32 || group == 64 || group == 128) && K % group == 0;
 }
@@ -1030,13 +1036,12 @@ int q4_make(const void* codes, const void* scales, const void* zeros, int64_t N,
     return code;
   };
   cudaError_t e;
-  const size_t data = round256(h->blob_bytes), tb = kQ4MaxTokens * 256 * sizeof(uint16_t);
-  if ((e = alloc_handle_memory(h, data + tb, st)) != cudaSuccess) return fail(cuda_status(e));
+  const size_t data = round256(h->blob_bytes), cb = q4_count_bytes(h);
+  if ((e = alloc_handle_memory(h, data + cb, st)) != cudaSuccess) return fail(cuda_status(e));
   h->q4.data = h->blob;
-  h->q4_t = reinterpret_cast<uint16_t*>(h->blob + data);
-  // t rows of tokens that no call has had yet are read (and their products dropped)
+  h->q4_count = reinterpret_cast<uint32_t*>(h->blob + data);
   if ((e = cudaMemsetAsync(h->status, 0, sizeof(int), st)) != cudaSuccess ||
-      (e = cudaMemsetAsync(h->q4_t, 0, tb, st)) != cudaSuccess)
+      (e = cudaMemsetAsync(h->q4_count, 0, cb, st)) != cudaSuccess)
     return fail(cuda_status(e));
   const long long words = N / 128 * (K / 64) * 1024;
   const unsigned grid = static_cast<unsigned>(std::min<long long>((words + 255) / 256, 16ll * device_sms(h->device)));
@@ -1921,6 +1926,7 @@ int salr_sync_status(salr_handle h, void* stream) {
     SALR_TRY(cudaMemset(h->sscr.tacc, 0, kTBuf * sizeof(float)));
     SALR_TRY(cudaMemset(h->sscr.tflags, 0, 2 * sizeof(uint32_t)));
   }
+  if (h->q4_count) SALR_TRY(cudaMemset(h->q4_count, 0, q4_count_bytes(h)));
   const int nrc = noalloc_reset(h->device);
   if (nrc != SALR_OK) return nrc;
   if (status & DEV_ERR_TIMEOUT) return SALR_ERR_TIMEOUT;

@@ -67,13 +67,35 @@ __device__ __forceinline__ uint32_t q4_bias(uint32_t pair, int hi) {
   return 0x43004300u | (((pair >> (8 * hi)) & 255u) * 0x00010001u);
 }
 
-__device__ __forceinline__ void mma_m16n8k16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                             uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+// d = a b + c over 16 x 8 x 16; without c, d = a b.
+__device__ __forceinline__ void mma_m16n8k16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_m16n8k16_zero(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+// The A fragments of the two products over 32 reduction steps, for 16 columns of an operand
+// that lies with its reduction index as row (64 columns, 128 bytes, to a row, 128-byte
+// swizzle; 16-byte chunk `col8` of the 64 columns and the next): ldmatrix turns 8 x 8
+// blocks, and its row addresses put the steps in the order of the X fragments.
+__device__ __forceinline__ void q4_turned(uint32_t tile, int step0, int col8, int lane, uint32_t (&a)[2][4]) {
+  const int mi = lane >> 3, kr = lane & 7;  // block, and its slot among the steps
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int row = step0 + 8 * (kr >> 1) + 4 * i + 2 * (mi >> 1) + (kr & 1);
+    const uint32_t ad = tile + row * 128 + (((col8 + (mi & 1)) ^ (row & 7)) << 4);
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(a[i][0]), "=r"(a[i][1]), "=r"(a[i][2]), "=r"(a[i][3])
+                 : "r"(ad)
+                 : "memory");
+  }
 }
 
 // 16 bytes that are read once, past L1.
@@ -86,93 +108,164 @@ __device__ __forceinline__ uint4 q4_stream16(const void* p) {
 }
 
 // ------------------------------------------------------------------------------------
-// t = X A for up to 64 tokens, summed in fp32 and stored as two bf16 parts, hi = bf16(t) and
-// lo = bf16(t - hi) (16 bits of significand): t2[m][64 (r / 32) + r % 32] = hi, lo 32 further
-// on; ranks past R up to a multiple of 32 are zero.  A cluster of CTAs takes 8 ranks and MT
-// tokens, each CTA a part of K: every thread multiplies rows k of A (16 bytes each), and the
-// parts meet in the first CTA's shared memory, all in a fixed order.
-constexpr int kQ4TThreads = 256;
-template <int MT>
-__global__ void __launch_bounds__(kQ4TThreads)
-    q4_t_kernel(const uint16_t* __restrict__ X, const uint16_t* __restrict__ A, int M, int K, int R,
-                int parts, uint16_t* __restrict__ t2) {
+// t = X A for up to 8 NT tokens, by one cluster of CTAs, each a part of K: stages of 64
+// columns of X and 64 rows of A (all ranks) by TMA, A read transposed (ldmatrix), a row tile
+// of 16 ranks a warp.  The fp32 sums meet in shared memory over the cluster, in order, and
+// are stored as two bf16 parts, hi = bf16(t) and lo = bf16(t - hi) (16 bits of significand):
+// t2[m][64 (r / 32) + r % 32] = hi, lo 32 further on.  Ranks past R are zero.
+//
+// One small cluster, so that the layer kernel beside it, which needs t at its end only, has
+// the machine: 128 ranks x 11008 columns are 2.8 MB, about 3 us for 8 SMs.
+constexpr int kQ4TParts = 8;
+constexpr int kQ4TWarps = 8;
+template <int NT>
+struct Q4TLayout {
+  static constexpr int kThreads = 32 * (kQ4TWarps + 1);
+  static constexpr int kStage = 16384 + NT * 1024;
+  // with four of them at NT = 4, a CTA would leave its SM room for one CTA of the layer kernel
+  // instead of two
+  static constexpr int kStages = NT == 4 ? 3 : 4;
+  static constexpr int kSmemBytes = kStages * kStage + 1024 + 256;
+  static constexpr int kSumRow = 132;  // floats: 128 ranks and a pad
+  static_assert(kStages * kStage >= NT * 8 * kSumRow * 4, "the stages hold the sums at the end");
+};
+
+struct Q4Ctrl {
+  uint64_t full[8], empty[8];
+  int abort;
+};
+
+__device__ __forceinline__ void q4_abort(int* status, Q4Ctrl* c) {
+  atomicOr(status, DEV_ERR_TIMEOUT);
+  *reinterpret_cast<volatile int*>(&c->abort) = 1;
+}
+__device__ __forceinline__ bool q4_aborted(Q4Ctrl* c) { return *reinterpret_cast<volatile int*>(&c->abort) != 0; }
+
+template <int NT>
+__global__ void __launch_bounds__(Q4TLayout<NT>::kThreads)
+    q4_t_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap ma, int M,
+                int K, int R, uint16_t* __restrict__ t2, int* status) {
+  using L = Q4TLayout<NT>;
   griddep_launch_dependents();  // the layer kernel waits for this grid before it reads t
-  __shared__ float warps[kQ4TThreads / 32][MT * 8];
-  __shared__ float sums[8][MT * 8];  // the first CTA's: one row a part
-  const int part = blockIdx.x % parts;
-  const int r0 = blockIdx.x / parts * 8, m0 = blockIdx.y * MT;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int k0 = static_cast<int>(static_cast<long long>(part) * K / parts);
-  const int k1 = static_cast<int>(static_cast<long long>(part + 1) * K / parts);
-  float acc[MT][8];
+  extern __shared__ uint8_t smem_raw[];
+  // the same offset in every CTA: dynamic shared memory starts alike in all of them
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  Q4Ctrl* ctrl = reinterpret_cast<Q4Ctrl*>(smem + L::kStages * L::kStage);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tl = lane & 3;
+  const int part = blockIdx.x, chunks = K / 64;
+  const int c0 = part * chunks / kQ4TParts, c1 = (part + 1) * chunks / kQ4TParts;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < L::kStages; ++s) {
+      mbar_init(&ctrl->full[s], 1);
+      mbar_init(&ctrl->empty[s], kQ4TWarps);
+    }
+    ctrl->abort = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  float acc[NT][4];
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
+  for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
+  if (warp == kQ4TWarps) {
+    if (lane == 0) {
+      int s = 0, ph = 0, issued = 0;
+      for (int c = c0; c < c1; ++c) {
+        if (!mbar_wait(&ctrl->empty[s], ph ^ 1) || q4_aborted(ctrl)) {
+          q4_abort(status, ctrl);
+          break;
+        }
+        uint8_t* a = smem + s * L::kStage;
+        uint64_t* bar = &ctrl->full[s];
+        mbar_arrive_expect_tx(bar, (R > 64 ? 16384 : 8192) + NT * 1024);
+        tma_load_2d(a, &ma, 0, c * 64, bar);
+        if (R > 64) tma_load_2d(a + 8192, &ma, 64, c * 64, bar);
+        tma_load_2d(a + 16384, &mx, c * 64, 0, bar);
+        ++issued;
+        if (++s == L::kStages) s = 0, ph ^= 1;
+      }
+      if (q4_aborted(ctrl))  // let the copies in flight land before the CTA can exit
+        for (int i = issued > L::kStages ? issued - L::kStages : 0; i < issued; ++i)
+          mbar_wait(&ctrl->full[i % L::kStages], (i / L::kStages) & 1);
+    }
+  } else {
+    const bool live = warp * 16 < R;
+    int s = 0, ph = 0;
+    for (int c = c0; c < c1; ++c) {
+      const bool ok = mbar_wait(&ctrl->full[s], ph);
+      if (!ok) q4_abort(status, ctrl);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      const uint8_t* tile = smem + s * L::kStage;
+      if (live) {
 #pragma unroll
-    for (int r = 0; r < 8; ++r) acc[m][r] = 0.f;
-  if (r0 < R) {
-#pragma unroll 2
-    for (int k = k0 + threadIdx.x; k < k1; k += kQ4TThreads) {
-      const uint4 a = *reinterpret_cast<const uint4*>(A + static_cast<size_t>(k) * R + r0);
-      float x[MT];
+        for (int h = 0; h < 2; ++h) {
+          uint32_t a[2][4];
+          q4_turned(smem_u32(tile) + (warp >> 2) * 8192, 32 * h, (warp & 3) * 2, lane, a);
+          const uint8_t* x = tile + 16384 + g * 128 + (((4 * h + tl) ^ g) << 4);
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
-        x[m] = m0 + m < M ? __uint_as_float(static_cast<uint32_t>(X[static_cast<size_t>(m0 + m) * K + k]) << 16) : 0.f;
-      const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float a0 = __uint_as_float(w[i] << 16), a1 = __uint_as_float(w[i] & 0xffff0000u);
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          acc[m][2 * i] = fmaf(x[m], a0, acc[m][2 * i]);
-          acc[m][2 * i + 1] = fmaf(x[m], a1, acc[m][2 * i + 1]);
+          for (int n = 0; n < NT; ++n) {
+            const uint4 v = *reinterpret_cast<const uint4*>(x + n * 1024);
+            mma_m16n8k16(acc[n], a[0], v.x, v.y);
+            mma_m16n8k16(acc[n], a[1], v.z, v.w);
+          }
         }
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctrl->empty[s]);
+      if (++s == L::kStages) s = 0, ph ^= 1;
     }
   }
+  __syncthreads();  // every stage has been used
+  float* sums = reinterpret_cast<float*>(smem);  // [8 NT tokens][132]
+  if (warp < kQ4TWarps) {
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int r = 0; r < 8; ++r) {
-      float v = acc[m][r];
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-      if (lane == 0) warps[warp][m * 8 + r] = v;
+    for (int n = 0; n < NT; ++n) {
+      float* d = sums + (8 * n + 2 * tl) * L::kSumRow + warp * 16 + g;
+      d[0] = acc[n][0];
+      d[L::kSumRow] = acc[n][1];
+      d[8] = acc[n][2];
+      d[L::kSumRow + 8] = acc[n][3];
     }
-  __syncthreads();
-  cluster_sync_all();  // every CTA of the cluster runs: its shared memory may be written
-  if (threadIdx.x < MT * 8) {
-    float v = 0.f;
-#pragma unroll
-    for (int w = 0; w < kQ4TThreads / 32; ++w) v += warps[w][threadIdx.x];
-    const uint32_t to = map_to_rank(smem_u32(&sums[part][threadIdx.x]), 0);
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to), "f"(v) : "memory");
   }
   __syncthreads();
   cluster_sync_all();
-  if (part == 0 && threadIdx.x < MT * 8) {
-    float v = 0.f;
-    for (int k = 0; k < parts; ++k) v += sums[k][threadIdx.x];
-    const int m = m0 + threadIdx.x / 8, r = r0 + threadIdx.x % 8;
-    const __nv_bfloat16 hi = __float2bfloat16_rn(v);
-    const float h = __bfloat162float(hi);
-    // an infinite value is all in hi
-    const __nv_bfloat16 lo = __float2bfloat16_rn(fabsf(h) <= 3.402823466e38f ? v - h : 0.f);
-    if (m < M) {
+  if (!q4_aborted(ctrl)) {
+    // this CTA's 16 ranks of every token
+    for (int i = threadIdx.x; i < M * 16; i += L::kThreads) {
+      const int m = i / 16, r = part * 16 + i % 16;
+      const uint32_t at = smem_u32(sums + m * L::kSumRow + r);
+      float v = 0.f;
+#pragma unroll
+      for (int k = 0; k < kQ4TParts; ++k) {
+        float x;
+        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(map_to_rank(at, k)));
+        v += x;
+      }
+      if (r >= R) v = 0.f;
+      const __nv_bfloat16 hi = __float2bfloat16_rn(v);
+      const float h = __bfloat162float(hi);
+      // an infinite value is all in hi
+      const __nv_bfloat16 lo = __float2bfloat16_rn(fabsf(h) <= 3.402823466e38f ? v - h : 0.f);
       uint16_t* o = t2 + m * 256 + r / 32 * 64 + r % 32;
       o[0] = *reinterpret_cast<const uint16_t*>(&hi);
       o[32] = *reinterpret_cast<const uint16_t*>(&lo);
     }
   }
+  __syncthreads();
+  cluster_sync_all();  // no CTA leaves while another may still read its sums
 }
 
 // ------------------------------------------------------------------------------------
-// The layer for M <= 8 NT tokens.  A cluster of CTAs takes a row block, each CTA a part of
-// its stages (128 columns).  One producer thread brings each stage's record by one bulk copy
-// and its X tiles by TMA (128-byte swizzle; tokens past M read as zero) into a ring; 8 / RT
-// consumer warps, RT row tiles each, rebuild the codes in registers and multiply.  After the
-// weight's stages come the adapter's, 32 ranks each: B by TMA, read transposed (ldmatrix), t
-// in its two parts from the t kernel.  The CTAs' sums meet in shared memory over the
-// cluster, in the order of the parts: results repeat bit for bit.
+// The layer for M <= 8 NT tokens.  Persistent CTAs, several to an SM: the weight's stages
+// (128 rows x 128 columns), row block by row block, are cut into one equal contiguous range
+// per CTA, so that every SM has the same work whatever the shape.  One producer thread
+// brings each stage's record by one bulk copy and its X tiles by TMA (128-byte swizzle;
+// tokens past M read as zero) into a ring; 8 / RT consumer warps, RT row tiles each, rebuild
+// the codes in registers and multiply.  The CTA whose range holds a row block's first stage
+// also takes the block's adapter, after its weight stages: 32 ranks a stage, B by TMA, read
+// transposed, t in its two parts.  A block that lies in one range is written at once;
+// otherwise each warp stores its fp32 sums and the last one to arrive for a row tile adds
+// them up in the order of the ranges: results repeat bit for bit.
 //
 // RT = 2 from 17 tokens on: a warp reads every X fragment once for its row tiles, and at 64
 // tokens one row tile a warp would read 16 bytes of X from shared memory per byte of codes.
@@ -183,60 +276,116 @@ struct Q4Layout {
   static constexpr int kThreads = 32 * (kWarps + 1);
   static constexpr int kXHalf = NT * 1024;  // 8 NT tokens x 64 columns
   static constexpr int kStage = 2 * kXHalf + 10240;
-  static constexpr int kStages = NT == 1 ? 5 : NT == 2 ? 5 : 4;
+  static constexpr int kStages = NT <= 2 ? 5 : 4;
   static constexpr int kSmemBytes = kStages * kStage + 1024 + 256;
-  static constexpr int kSumRow = 132;  // floats: 128 rows and a pad
-  static_assert(kQ4MaxRecord <= 10240 && kStages * kStage >= NT * 8 * kSumRow * 4, "stage sizes");
-};
-
-struct Q4Ctrl {
-  uint64_t full[8], empty[8];
-  int abort;
+  static_assert(kQ4MaxRecord <= 10240, "a record fits its stage");
+  // CTAs per SM that the shared memory admits (1 KB of it is the system's, per CTA)
+  static constexpr int kPerSm = 233472 / (kSmemBytes + 1024) > 4 ? 4 : 233472 / (kSmemBytes + 1024);
 };
 
 struct Q4Params {
   Q4View w;
   uint16_t* Y;
+  float* part;      // [2 CTAs][M][128]: a CTA's range has at most two blocks it shares
+  uint32_t* count;  // [blocks][8 row tiles] arrivals, zero between calls
   int* status;
   int M, R;
-  int parts;   // CTAs of a cluster
+  int stages;       // of a row block
+  long long total;  // stages in all
 };
 
-__device__ __forceinline__ uint4 q4_lds16(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
-  return v;
+// First stage of CTA c's range, of `ctas`; and the CTA whose range holds stage i.
+__device__ __forceinline__ long long q4_range(long long total, int c, int ctas) { return total * c / ctas; }
+__device__ __forceinline__ int q4_owner(long long total, long long i, int ctas) {
+  return static_cast<int>(((i + 1) * ctas - 1) / total);
 }
-__device__ __forceinline__ uint32_t q4_lds4(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ uint32_t q4_lds2(uint32_t a) {
-  uint16_t v;
-  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
-  return v;
+
+// One stage of COLS columns of the weight into the sums.
+template <int NT, int GROUP, bool ZEROS, int COLS>
+__device__ __forceinline__ void q4_stage(const uint8_t* x, const uint8_t* rec, int warp, int lane,
+                                         float (&acc)[Q4Layout<NT>::RT][NT][4]) {
+  using L = Q4Layout<NT>;
+  constexpr int RT = L::RT;
+  const int g = lane >> 2, tl = lane & 3;
+  const uint8_t* codes = rec + warp * (RT * 512) + lane * 16;
+  const uint8_t* scales = rec + 64 * COLS + (warp * RT * 8 + g) * 4;
+  const uint8_t* zeros = rec + 64 * COLS + COLS / GROUP * 256 + (warp * RT * 8 + g) * 2;
+  // token 8n + g, 16-byte chunks tl and 4 + tl of its 64 columns, swizzled
+  const uint8_t* const xh[2] = {x + g * 128 + ((tl ^ g) << 4), x + g * 128 + (((4 + tl) ^ g) << 4)};
+  float cc[RT][NT][4];
+#pragma unroll
+  for (int b = 0; b < COLS / 64; ++b) {
+    uint4 code[RT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) code[r] = *reinterpret_cast<const uint4*>(codes + b * 4096 + r * 512);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {  // 32 columns, two products
+      const int grp = (b * 64 + h * 32) / GROUP;
+      const bool first = (b * 64 + h * 32) % GROUP == 0;
+      const bool end = (b * 64 + h * 32 + 32) % GROUP == 0;
+      uint32_t a[RT][2][4];
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        uint32_t lo = 0x43084308u, hi = 0x43084308u;
+        if (ZEROS) {
+          const uint32_t z = *reinterpret_cast<const uint16_t*>(zeros + grp * 128 + r * 16);
+          lo = q4_bias(z, 0);
+          hi = q4_bias(z, 1);
+        }
+        const uint32_t w0 = h ? code[r].y : code[r].x, w1 = h ? code[r].w : code[r].z;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int sh = 4 * (2 * i + j);
+            a[r][i][2 * j] = q4_sub2(((w0 >> sh) & 0x000f000fu) | 0x43004300u, lo);
+            a[r][i][2 * j + 1] = q4_sub2(((w1 >> sh) & 0x000f000fu) | 0x43004300u, hi);
+          }
+      }
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const uint4 v = *reinterpret_cast<const uint4*>(xh[h] + b * L::kXHalf + n * 1024);
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+          if (first)
+            mma_m16n8k16_zero(cc[r][n], a[r][0], v.x, v.y);
+          else
+            mma_m16n8k16(cc[r][n], a[r][0], v.x, v.y);
+          mma_m16n8k16(cc[r][n], a[r][1], v.z, v.w);
+        }
+      }
+      if (end) {
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+          const uint32_t s2 = *reinterpret_cast<const uint32_t*>(scales + grp * 256 + r * 32);
+          const float sl = __uint_as_float(s2 << 16), sh = __uint_as_float(s2 & 0xffff0000u);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            acc[r][n][0] = fmaf(sl, cc[r][n][0], acc[r][n][0]);
+            acc[r][n][1] = fmaf(sl, cc[r][n][1], acc[r][n][1]);
+            acc[r][n][2] = fmaf(sh, cc[r][n][2], acc[r][n][2]);
+            acc[r][n][3] = fmaf(sh, cc[r][n][3], acc[r][n][3]);
+          }
+        }
+      }
+    }
+  }
 }
 
 template <int NT, int GROUP, bool ZEROS>
-__global__ void __launch_bounds__(Q4Layout<NT>::kThreads)
+__global__ void __launch_bounds__(Q4Layout<NT>::kThreads, Q4Layout<NT>::kPerSm)
     q4_linear_kernel(const __grid_constant__ Q4Params p, const __grid_constant__ CUtensorMap mx,
                      const __grid_constant__ CUtensorMap mt, const __grid_constant__ CUtensorMap mb) {
   using L = Q4Layout<NT>;
   constexpr int RT = L::RT;
   extern __shared__ uint8_t smem_raw[];
-  // the same offset in every CTA: dynamic shared memory starts alike in all of them
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   Q4Ctrl* ctrl = reinterpret_cast<Q4Ctrl*>(smem + L::kStages * L::kStage);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int part = blockIdx.x % p.parts, block = blockIdx.x / p.parts;
-  const int stages = (p.w.K + kQ4Cols - 1) / kQ4Cols, ranks = (p.R + 31) / 32;
-  const int s0 = static_cast<int>(static_cast<long long>(part) * stages / p.parts);
-  const int s1 = static_cast<int>(static_cast<long long>(part + 1) * stages / p.parts);
-  // the adapter's stages are shared out as well
-  const int a0 = part * ranks / p.parts, a1 = (part + 1) * ranks / p.parts;
-  volatile int* abort_flag = &ctrl->abort;
+  const int cta = blockIdx.x, ctas = gridDim.x;
+  const long long i0 = q4_range(p.total, cta, ctas), i1 = q4_range(p.total, cta + 1, ctas);
+  const int ranks = (p.R + 31) / 32;  // adapter stages of a block
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < L::kStages; ++s) {
@@ -248,203 +397,143 @@ __global__ void __launch_bounds__(Q4Layout<NT>::kThreads)
   }
   __syncthreads();
 
-  float acc[RT][NT][4];
-#pragma unroll
-  for (int r = 0; r < RT; ++r)
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[r][n][i] = 0.f;
-
   if (warp == L::kWarps) {
     if (lane == 0) {
       int s = 0, ph = 0, issued = 0;
-      for (int c = s0; c < s1 + a1 - a0; ++c) {
-        if (!mbar_wait(&ctrl->empty[s], ph ^ 1) || *abort_flag) {
-          atomicOr(p.status, DEV_ERR_TIMEOUT);
-          *abort_flag = 1;
-          break;
+      bool ok = true, waited = false;
+      for (long long i = i0; i < i1 && ok;) {
+        const int block = static_cast<int>(i / p.stages), c0 = static_cast<int>(i - static_cast<long long>(block) * p.stages);
+        const int n = static_cast<int>(min(static_cast<long long>(p.stages - c0), i1 - i));
+        const int extra = c0 == 0 ? ranks : 0;
+        for (int c = 0; c < n + extra; ++c) {
+          if (!mbar_wait(&ctrl->empty[s], ph ^ 1) || q4_aborted(ctrl)) {
+            q4_abort(p.status, ctrl);
+            ok = false;
+            break;
+          }
+          uint8_t* x = smem + s * L::kStage;
+          uint8_t* rec = x + 2 * L::kXHalf;
+          uint64_t* bar = &ctrl->full[s];
+          if (c < n) {
+            const int col = (c0 + c) * kQ4Cols, cols = min(kQ4Cols, p.w.K - col);
+            const uint32_t bytes = static_cast<uint32_t>(p.w.record(cols));
+            mbar_arrive_expect_tx(bar, bytes + cols / 64 * L::kXHalf);
+            bulk_g2s(rec, p.w.at(block, c0 + c), bytes, bar);
+            tma_load_2d(x, &mx, col, 0, bar);
+            if (cols > 64) tma_load_2d(x + L::kXHalf, &mx, col + 64, 0, bar);
+          } else {
+            const int a = c - n;
+            if (!waited) griddep_wait();  // t
+            waited = true;
+            mbar_arrive_expect_tx(bar, 8192 + L::kXHalf);
+            tma_load_2d(rec, &mb, block * 128, a * 32, bar);
+            tma_load_2d(rec + 4096, &mb, block * 128 + 64, a * 32, bar);
+            tma_load_2d(x, &mt, a * 64, 0, bar);
+          }
+          ++issued;
+          if (++s == L::kStages) s = 0, ph ^= 1;
         }
-        uint8_t* x = smem + s * L::kStage;
-        uint8_t* rec = x + 2 * L::kXHalf;
-        uint64_t* bar = &ctrl->full[s];
-        if (c < s1) {
-          const int cols = min(kQ4Cols, p.w.K - c * kQ4Cols);
-          const uint32_t bytes = static_cast<uint32_t>(p.w.record(cols));
-          mbar_arrive_expect_tx(bar, bytes + cols / 64 * L::kXHalf);
-          bulk_g2s(rec, p.w.at(block, c), bytes, bar);
-          tma_load_2d(x, &mx, c * kQ4Cols, 0, bar);
-          if (cols > 64) tma_load_2d(x + L::kXHalf, &mx, c * kQ4Cols + 64, 0, bar);
-        } else {
-          const int a = a0 + c - s1;
-          if (c == s1) griddep_wait();  // t
-          mbar_arrive_expect_tx(bar, 8192 + L::kXHalf);
-          tma_load_2d(rec, &mb, block * 128, a * 32, bar);
-          tma_load_2d(rec + 4096, &mb, block * 128 + 64, a * 32, bar);
-          tma_load_2d(x, &mt, a * 64, 0, bar);
-        }
-        ++issued;
-        if (++s == L::kStages) s = 0, ph ^= 1;
+        i += n;
       }
-      if (*abort_flag)  // let the copies in flight land before the CTA can exit
-        for (int i = issued > L::kStages ? issued - L::kStages : 0; i < issued; ++i)
-          mbar_wait(&ctrl->full[i % L::kStages], (i / L::kStages) & 1);
+      if (q4_aborted(ctrl))  // let the copies in flight land before the CTA can exit
+        for (int k = issued > L::kStages ? issued - L::kStages : 0; k < issued; ++k)
+          mbar_wait(&ctrl->full[k % L::kStages], (k / L::kStages) & 1);
+      if (p.R > 0 && !waited) griddep_wait();  // this grid ends after the t kernel
     }
-  } else {
-    const int g = lane >> 2, tl = lane & 3;
-    // this lane's X addresses within a half: token 8n + g, 16-byte chunk (4 h + tl), swizzled
-    const uint32_t xrow = static_cast<uint32_t>(g * 128);
-    const uint32_t xc[2] = {xrow + ((static_cast<uint32_t>(tl) ^ g) << 4),
-                            xrow + ((static_cast<uint32_t>(4 + tl) ^ g) << 4)};
-    int s = 0, ph = 0;
-    bool ok = true;
-    for (int c = s0; c < s1 + a1 - a0; ++c) {
-      ok = mbar_wait(&ctrl->full[s], ph) && !*abort_flag;
-      if (!ok) {
-        atomicOr(p.status, DEV_ERR_TIMEOUT);
-        *abort_flag = 1;
+    return;
+  }
+
+  const int g = lane >> 2, tl = lane & 3;
+  int s = 0, ph = 0;
+  for (long long i = i0; i < i1;) {
+    const int block = static_cast<int>(i / p.stages), c0 = static_cast<int>(i - static_cast<long long>(block) * p.stages);
+    const int n = static_cast<int>(min(static_cast<long long>(p.stages - c0), i1 - i));
+    const int extra = c0 == 0 ? ranks : 0;
+    float acc[RT][NT][4];
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int k = 0; k < NT; ++k) acc[r][k][0] = acc[r][k][1] = acc[r][k][2] = acc[r][k][3] = 0.f;
+    for (int c = 0; c < n + extra; ++c) {
+      const bool ok = mbar_wait(&ctrl->full[s], ph);
+      if (!__all_sync(0xffffffffu, ok)) {
+        q4_abort(p.status, ctrl);
+        return;
       }
-      if (!__all_sync(0xffffffffu, ok)) break;
-      const uint32_t x = smem_u32(smem + s * L::kStage), rec = x + 2 * L::kXHalf;
-      if (c < s1) {
-        const int cols = min(kQ4Cols, p.w.K - c * kQ4Cols);
-        const uint32_t sc0 = rec + 64 * cols, zp0 = sc0 + cols / GROUP * 256;
-        float cc[RT][NT][4];
+      const uint8_t* x = smem + s * L::kStage;
+      const uint8_t* rec = x + 2 * L::kXHalf;
+      if (c < n) {
+        if (GROUP == 128 || p.w.K - (c0 + c) * kQ4Cols >= kQ4Cols)
+          q4_stage<NT, GROUP, ZEROS, kQ4Cols>(x, rec, warp, lane, acc);
+        else
+          q4_stage<NT, GROUP, ZEROS, GROUP == 128 ? 128 : 64>(x, rec, warp, lane, acc);
+      } else {
+        uint32_t a[RT][2][4];
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          if (b * 64 >= cols) break;
-          uint4 code[RT];
+        for (int r = 0; r < RT; ++r) {
+          const int row = (warp * RT + r) * 16;
+          q4_turned(smem_u32(rec) + (row >> 6) * 4096, 0, (row & 63) >> 3, lane, a[r]);
+        }
 #pragma unroll
-          for (int r = 0; r < RT; ++r)
-            code[r] = q4_lds16(rec + b * 4096 + (warp * RT + r) * 512 + lane * 16);
+        for (int h = 0; h < 2; ++h)  // t's two parts
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {  // 32 columns, two products
-            const int grp = (b * 64 + h * 32) / GROUP;
-            const bool first = (b * 64 + h * 32) % GROUP == 0;
-            const bool end = (b * 64 + h * 32 + 32) % GROUP == 0;
-            uint32_t a[RT][2][4];
+          for (int k = 0; k < NT; ++k) {
+            const uint4 v = *reinterpret_cast<const uint4*>(x + k * 1024 + g * 128 + (((4 * h + tl) ^ g) << 4));
 #pragma unroll
             for (int r = 0; r < RT; ++r) {
-              const uint32_t at = (grp * 8 + warp * RT + r) * 8 + g;
-              uint32_t lo = 0x43084308u, hi = 0x43084308u;
-              if (ZEROS) {
-                const uint32_t z = q4_lds2(zp0 + at * 2);
-                lo = q4_bias(z, 0);
-                hi = q4_bias(z, 1);
-              }
-              const uint32_t w0 = h ? code[r].y : code[r].x, w1 = h ? code[r].w : code[r].z;
-#pragma unroll
-              for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                  const int sh = 4 * (2 * i + j);
-                  a[r][i][2 * j] = q4_sub2(((w0 >> sh) & 0x000f000fu) | 0x43004300u, lo);
-                  a[r][i][2 * j + 1] = q4_sub2(((w1 >> sh) & 0x000f000fu) | 0x43004300u, hi);
-                }
-            }
-            float sl[RT], sh[RT];
-            if (end) {
-#pragma unroll
-              for (int r = 0; r < RT; ++r) {
-                const uint32_t s2 = q4_lds4(sc0 + ((grp * 8 + warp * RT + r) * 8 + g) * 4);
-                sl[r] = __uint_as_float(s2 << 16);
-                sh[r] = __uint_as_float(s2 & 0xffff0000u);
-              }
-            }
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              const uint4 v = q4_lds16(x + b * L::kXHalf + n * 1024 + xc[h]);
-#pragma unroll
-              for (int r = 0; r < RT; ++r) {
-                float(&d)[4] = cc[r][n];
-                if (first) d[0] = d[1] = d[2] = d[3] = 0.f;
-                mma_m16n8k16(d, a[r][0][0], a[r][0][1], a[r][0][2], a[r][0][3], v.x, v.y);
-                mma_m16n8k16(d, a[r][1][0], a[r][1][1], a[r][1][2], a[r][1][3], v.z, v.w);
-                if (end) {
-                  acc[r][n][0] = fmaf(sl[r], d[0], acc[r][n][0]);
-                  acc[r][n][1] = fmaf(sl[r], d[1], acc[r][n][1]);
-                  acc[r][n][2] = fmaf(sh[r], d[2], acc[r][n][2]);
-                  acc[r][n][3] = fmaf(sh[r], d[3], acc[r][n][3]);
-                }
-              }
+              mma_m16n8k16(acc[r][k], a[r][0], v.x, v.y);
+              mma_m16n8k16(acc[r][k], a[r][1], v.z, v.w);
             }
           }
-        }
-      } else {
-        // 32 ranks: B is [rank][64 rows] twice, 128-byte swizzled.  ldmatrix turns 8 ranks x
-        // 8 rows; its row addresses put the ranks in the order of the t fragments.
-        const int mi = lane >> 3, kr = lane & 7;  // matrix, and its k slot
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          uint32_t a[RT][4];
-#pragma unroll
-          for (int r = 0; r < RT; ++r) {
-            const int rank = 8 * (kr >> 1) + 4 * i + 2 * (mi >> 1) + (kr & 1);
-            const int row = (warp * RT + r) * 16 + 8 * (mi & 1);
-            const uint32_t ad = rec + (row >> 6) * 4096 + rank * 128 +
-                                ((static_cast<uint32_t>((row & 63) >> 3) ^ (rank & 7)) << 4);
-            asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-                         : "=r"(a[r][0]), "=r"(a[r][1]), "=r"(a[r][2]), "=r"(a[r][3])
-                         : "r"(ad));
-          }
-#pragma unroll
-          for (int h = 0; h < 2; ++h)  // t's two parts
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              const uint4 v = q4_lds16(x + n * 1024 + xc[h]);
-#pragma unroll
-              for (int r = 0; r < RT; ++r)
-                mma_m16n8k16(acc[r][n], a[r][0], a[r][1], a[r][2], a[r][3], i ? v.z : v.x, i ? v.w : v.y);
-            }
-        }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctrl->empty[s]);
       if (++s == L::kStages) s = 0, ph ^= 1;
     }
-  }
-  __syncthreads();  // every stage has been used
-  float* sums = reinterpret_cast<float*>(smem);  // [8 NT tokens][132]
-  if (warp < L::kWarps) {
-    const int g = lane >> 2, tl = lane & 3;
+    if (q4_aborted(ctrl)) return;  // the values are not whole: nothing of the block is written
+    // this warp's rows of the block: values (row, token) at 4 places of each 16 x 8 tile
+    const size_t n0 = static_cast<size_t>(block) * 128;
+    auto each = [&](auto&& f) {
 #pragma unroll
-    for (int r = 0; r < RT; ++r)
+      for (int r = 0; r < RT; ++r)
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        float* d = sums + (8 * n + 2 * tl) * L::kSumRow + (warp * RT + r) * 16 + g;
-        d[0] = acc[r][n][0];
-        d[L::kSumRow] = acc[r][n][1];
-        d[8] = acc[r][n][2];
-        d[L::kSumRow + 8] = acc[r][n][3];
-      }
-  }
-  __syncthreads();
-  if (p.parts > 1) cluster_sync_all();
-  if (*abort_flag == 0) {
-    const int rows = 128 / p.parts, r0 = part * rows;
-    const uint32_t base = smem_u32(sums);
-    for (int i = threadIdx.x; i < p.M * (rows / 2); i += L::kThreads) {
-      const int m = i / (rows / 2), row = r0 + i % (rows / 2) * 2;
-      const uint32_t at = base + (m * L::kSumRow + row) * 4;
-      float v0 = 0.f, v1 = 0.f;
+        for (int k = 0; k < NT; ++k)
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (k < p.parts) {
-          float x0, x1;
-          asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
-                       : "=f"(x0), "=f"(x1)
-                       : "r"(map_to_rank(at, k)));
-          v0 += x0;
-          v1 += x1;
+          for (int e = 0; e < 4; ++e) {
+            const int m = 8 * k + 2 * tl + (e & 1), row = (warp * RT + r) * 16 + g + 8 * (e >> 1);
+            if (m < p.M) f(acc[r][k][e], m, row);
+          }
+    };
+    auto store = [&](float v, int m, int row) {
+      reinterpret_cast<__nv_bfloat16*>(p.Y)[static_cast<size_t>(m) * p.w.N + n0 + row] = __float2bfloat16_rn(v);
+    };
+    if (n == p.stages) {
+      each(store);
+    } else {
+      const size_t slot = static_cast<size_t>(p.M) * 128;
+      // a block that the range starts in takes the CTA's slot 0, one that it ends in slot 1
+      float* mine = p.part + (2 * static_cast<size_t>(cta) + (i == i0 ? 0 : 1)) * slot;
+      each([&](float v, int m, int row) { __stcg(mine + m * 128 + row, v); });
+      __threadfence();
+      __syncwarp();
+      const long long b0 = static_cast<long long>(block) * p.stages;
+      const int f = q4_owner(p.total, b0, ctas), l = q4_owner(p.total, b0 + p.stages - 1, ctas);
+      uint32_t last = 0;
+      if (lane == 0) last = atomicAdd(p.count + block * 8 + warp, 1u) == static_cast<uint32_t>(l - f);
+      if (__shfl_sync(0xffffffffu, last, 0)) {
+        __threadfence();
+        // the first CTA of the block has it in slot 1 unless its range starts with the block
+        const float* from = p.part + (2 * static_cast<size_t>(f) + (q4_range(p.total, f, ctas) == b0 ? 0 : 1)) * slot;
+        each([&](float& v, int m, int row) { v = __ldcg(from + m * 128 + row); });
+        for (int c = f + 1; c <= l; ++c) {
+          const float* next = p.part + 2 * static_cast<size_t>(c) * slot;
+          each([&](float& v, int m, int row) { v += __ldcg(next + m * 128 + row); });
         }
-      *reinterpret_cast<__nv_bfloat162*>(p.Y + static_cast<size_t>(m) * p.w.N + block * 128 + row) =
-          __floats2bfloat162_rn(v0, v1);
+        each(store);
+        if (lane == 0) p.count[block * 8 + warp] = 0u;
+      }
     }
-  }
-  if (p.R > 0 && threadIdx.x == 0) griddep_wait();  // this grid ends after the t kernel
-  if (p.parts > 1) {
-    __syncthreads();
-    cluster_sync_all();  // no CTA leaves while another may still read its sums
+    i += n;
   }
 }
 
