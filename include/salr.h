@@ -367,7 +367,9 @@ SALR_API int salr_residual_adapter(const void* W, salr_handle h, int64_t r, cons
  * once) and the rest is as described under salr_linear.  The handle must be on the current
  * device (else SALR_ERR_INVALID); its arrival counts (M <= 64) are not safe to share between
  * calls that run concurrently on different streams, captured graphs among them.  Scratch
- * (t and partial sums) is the call's own, from the library's pool.
+ * (t and partial sums) is the call's own, from the library's pool.  As described for M <= 64
+ * under salr_linear, the call may start while the previous kernel on `stream` is still
+ * running; before that has completed it reads only the handle's packed weight.
  */
 SALR_API int salr_q4_pack(const void* codes, const void* scales, const void* zeros, int64_t N,
                           int64_t K, int64_t group, void* stream, salr_handle* out);

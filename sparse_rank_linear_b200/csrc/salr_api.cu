@@ -213,6 +213,21 @@ bool make_map(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// A row-major bf16 matrix [outer x inner] as blocks of 64 columns, [inner / 64][outer][64],
+// 128-byte swizzle: a box is `box_blocks` blocks of `box_outer` rows.
+bool make_block_map(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint32_t box_outer,
+                    uint32_t box_blocks) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {64, outer, inner / 64};
+  cuuint64_t strides[2] = {inner * 2, 128};
+  cuuint32_t box[3] = {64, box_outer, box_blocks};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
+             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 void release(salr_weight_s* h) {
   int cur = -1;
   const bool switched = cudaGetDevice(&cur) == cudaSuccess && cur != h->device &&
@@ -714,9 +729,10 @@ int check_linear_args(const void* X, int64_t M, salr_handle h, const void* A, co
   return SALR_OK;
 }
 
-// Fewest stages of a CTA's range (below, its set-up and the sums' meeting cost more than
-// the stages).
-constexpr int kQ4MinStages = 4;
+// Fewest records of a CTA's range (below, its set-up and the sums' meeting cost more than
+// the records).
+constexpr int kQ4MinRecords = 4;
+constexpr int kQ4LongRange = 16;
 
 template <int NT, int GROUP, bool ZEROS>
 int launch_q4_kernel(const Q4Params& p, const CUtensorMap* m, int ctas, int dev, cudaStream_t st) {
@@ -732,13 +748,14 @@ int launch_q4_kernel(const Q4Params& p, const CUtensorMap* m, int ctas, int dev,
   cfg.blockDim = dim3(L::kThreads);
   cfg.dynamicSmemBytes = L::kSmemBytes;
   cfg.stream = st;
-  // Directly after the t kernel, the launch may overlap it: records, X and B were complete
-  // before that kernel started, and t is waited for.
+  // The launch may overlap the kernel ahead.  After the t kernel: records, X and B are
+  // complete once that kernel lets this one start, and t is waited for.  Else: only records
+  // are read before the kernel ahead has completed.
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = p.R > 0 ? 1 : 0;
+  cfg.numAttrs = 1;
   SALR_TRY(cudaLaunchKernelEx(&cfg, kern, p, m[0], m[1], m[2]));
   return SALR_OK;
 }
@@ -757,12 +774,14 @@ int launch_q4_t(const CUtensorMap& mx, const CUtensorMap& ma, int M, int K, int 
   cfg.blockDim = dim3(L::kThreads);
   cfg.dynamicSmemBytes = L::kSmemBytes;
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = kQ4TParts;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   SALR_TRY(cudaLaunchKernelEx(&cfg, q4_t_kernel<NT>, mx, ma, M, K, R, t, status));
   return SALR_OK;
 }
@@ -782,17 +801,25 @@ int launch_q4(const void* X, int M, salr_handle h, const void* A, const void* B,
   p.status = h->status;
   p.M = M;
   p.R = R;
-  p.stages = (K + kQ4Cols - 1) / kQ4Cols;
-  p.total = static_cast<long long>(blocks) * p.stages;
-  // every CTA resident at once, the t kernel's beside them
-  const long long slots = static_cast<long long>(Q4Layout<NT>::kPerSm) * device_sms(dev) - (R > 0 ? kQ4TParts : 0);
-  const int ctas = static_cast<int>(std::max<long long>(1, std::min(slots, p.total / kQ4MinStages)));
-  CUtensorMap m[3], ma;
+  p.records = (K + kQ4Cols - 1) / kQ4Cols;
+  p.total = static_cast<long long>(blocks) * p.records;
+  // Every CTA resident at once, the t kernel's beside them.  Equal ranges of the records; but
+  // where those are short (under kQ4LongRange records), every block is cut alike into as many
+  // parts as leave all CTAs resident: a CTA then has one sum to hand over, not two.
+  const int sms = device_sms(dev);
+  const long long beside = R > 0 ? kQ4TParts * ((Q4TLayout<NT>::kSmemBytes + Q4Layout<NT>::kSmemBytes - 1) /
+                                                Q4Layout<NT>::kSmemBytes) : 0;
+  const long long slots = std::max<long long>(1, static_cast<long long>(Q4Layout<NT>::kPerSm) * sms - beside);
+  const long long most = std::max<long long>(1, p.total / kQ4MinRecords);
+  long long grid = std::min(slots, most);
+  if (p.total / grid < kQ4LongRange && blocks <= grid) grid = grid / blocks * blocks;
+  const int ctas = static_cast<int>(grid);
+  CUtensorMap m[3], ma, mx;
   std::memset(m, 0, sizeof(m));
-  if (!make_map(&m[0], X, K, M, 64, 8 * NT)) return SALR_ERR_CUDA;
+  if (!make_block_map(&m[0], X, K, M, 8 * NT, 2 * Q4Layout<NT>::kRecords)) return SALR_ERR_CUDA;
   // scratch: [t][partial sums], where there are any
   const size_t tb = R > 0 ? kQ4MaxTokens * 256 * sizeof(uint16_t) : 0;
-  const bool shared = p.total % ctas != 0 || (p.total / ctas) % p.stages != 0;
+  const bool shared = p.total % ctas != 0 || (p.total / ctas) % p.records != 0;
   const size_t pb = shared ? 2 * static_cast<size_t>(ctas) * M * 128 * sizeof(float) : 0;
   uint8_t* mem = nullptr;
   if (tb + pb) SALR_TRY(dev_alloc_async(reinterpret_cast<void**>(&mem), tb + pb, st, kPoolScratch));
@@ -802,9 +829,9 @@ int launch_q4(const void* X, int M, salr_handle h, const void* A, const void* B,
       // t rows past M are not written: their products belong to no token
       uint16_t* t = reinterpret_cast<uint16_t*>(mem);
       if (!make_map(&m[1], t, 256, M, 64, 8 * NT) || !make_map(&m[2], B, h->N, R, 64, 32) ||
-          !make_map(&ma, A, R, K, 64, 64))
+          !make_block_map(&mx, X, K, M, 8 * NT, 2) || !make_map(&ma, A, R, K, 64, 128))
         return SALR_ERR_CUDA;
-      const int rc = launch_q4_t<NT>(m[0], ma, M, K, R, t, h->status, dev, st);
+      const int rc = launch_q4_t<NT>(mx, ma, M, K, R, t, h->status, dev, st);
       if (rc != SALR_OK) return rc;
     }
     const int g = h->group;

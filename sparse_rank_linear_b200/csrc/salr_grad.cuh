@@ -31,6 +31,11 @@
 
 namespace salr {
 
+// The next 1024-byte boundary of shared memory, by an offset: rounding the pointer itself
+// would hide from the compiler that it is shared memory, and cost 64-bit addresses and
+// generic loads.
+__device__ __forceinline__ uint8_t* align_1024(uint8_t* p) { return p + ((0u - smem_u32(p)) & 1023u); }
+
 // ---------------------------------------------------------------- CTA-pair wrappers
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -163,8 +168,7 @@ __global__ void __launch_bounds__(kGradThreads)
   using L = GradSkinny<BN>;
   extern __shared__ uint8_t smem_raw[];
   // the same offset in every CTA: dynamic shared memory starts alike in all of them
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~static_cast<uintptr_t>(1023));
+  uint8_t* smem = align_1024(smem_raw);
   GradCtrl* ctrl = reinterpret_cast<GradCtrl*>(smem + L::kStages * L::kStage);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int part = blockIdx.x % nc, all = blockIdx.x / nc;
@@ -416,8 +420,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
                    const __grid_constant__ CUtensorMap ma) {
   extern __shared__ uint8_t smem_raw[];
   // the same offset in both CTAs: dynamic shared memory starts alike in every CTA
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~static_cast<uintptr_t>(1023));
+  uint8_t* smem = align_1024(smem_raw);
   GradDxCtrl* ctrl = reinterpret_cast<GradDxCtrl*>(smem + kDxStages * kDxStage);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();

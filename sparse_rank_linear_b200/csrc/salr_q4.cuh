@@ -62,6 +62,19 @@ __device__ __forceinline__ uint32_t q4_sub2(uint32_t a, uint32_t b) {
   asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
+// (w & 0x000f000f) | 0x43004300 in one instruction: the constants come in registers (given
+// as literals, the compiler spends one instruction on each).
+__device__ __forceinline__ uint32_t q4_pair(uint32_t w, uint32_t mask, uint32_t one28) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(d) : "r"(w), "r"(mask), "r"(one28));
+  return d;
+}
+// A constant the compiler cannot see through.
+__device__ __forceinline__ uint32_t q4_opaque(uint32_t c) {
+  uint32_t d;
+  asm volatile("mov.u32 %0, %1;" : "=r"(d) : "r"(c));
+  return d;
+}
 // (128 + z) twice, from byte `hi` of a pair of zero points
 __device__ __forceinline__ uint32_t q4_bias(uint32_t pair, int hi) {
   return 0x43004300u | (((pair >> (8 * hi)) & 255u) * 0x00010001u);
@@ -107,9 +120,19 @@ __device__ __forceinline__ uint4 q4_stream16(const void* p) {
   return v;
 }
 
+// Tiled 3-D tensor copy global -> shared (c0 in elements, a multiple of 16 bytes).
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int32_t c0, int32_t c1,
+                                            int32_t c2, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
+      : "memory");
+}
+
 // ------------------------------------------------------------------------------------
-// t = X A for up to 8 NT tokens, by one cluster of CTAs, each a part of K: stages of 64
-// columns of X and 64 rows of A (all ranks) by TMA, A read transposed (ldmatrix), a row tile
+// t = X A for up to 8 NT tokens, by one cluster of CTAs, each a part of K: stages of 128
+// columns of X and 128 rows of A (all ranks) by TMA, A read transposed (ldmatrix), a row tile
 // of 16 ranks a warp.  The fp32 sums meet in shared memory over the cluster, in order, and
 // are stored as two bf16 parts, hi = bf16(t) and lo = bf16(t - hi) (16 bits of significand):
 // t2[m][64 (r / 32) + r % 32] = hi, lo 32 further on.  Ranks past R are zero.
@@ -121,10 +144,8 @@ constexpr int kQ4TWarps = 8;
 template <int NT>
 struct Q4TLayout {
   static constexpr int kThreads = 32 * (kQ4TWarps + 1);
-  static constexpr int kStage = 16384 + NT * 1024;
-  // with four of them at NT = 4, a CTA would leave its SM room for one CTA of the layer kernel
-  // instead of two
-  static constexpr int kStages = NT == 4 ? 3 : 4;
+  static constexpr int kStage = 32768 + NT * 2048;
+  static constexpr int kStages = NT <= 4 ? 4 : 3;  // about 130 KB in flight
   static constexpr int kSmemBytes = kStages * kStage + 1024 + 256;
   static constexpr int kSumRow = 132;  // floats: 128 ranks and a pad
   static_assert(kStages * kStage >= NT * 8 * kSumRow * 4, "the stages hold the sums at the end");
@@ -146,14 +167,12 @@ __global__ void __launch_bounds__(Q4TLayout<NT>::kThreads)
     q4_t_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap ma, int M,
                 int K, int R, uint16_t* __restrict__ t2, int* status) {
   using L = Q4TLayout<NT>;
-  griddep_launch_dependents();  // the layer kernel waits for this grid before it reads t
   extern __shared__ uint8_t smem_raw[];
   // the same offset in every CTA: dynamic shared memory starts alike in all of them
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~static_cast<uintptr_t>(1023));
+  uint8_t* smem = align_1024(smem_raw);
   Q4Ctrl* ctrl = reinterpret_cast<Q4Ctrl*>(smem + L::kStages * L::kStage);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tl = lane & 3;
-  const int part = blockIdx.x, chunks = K / 64;
+  const int part = blockIdx.x, chunks = (K + 127) / 128;
   const int c0 = part * chunks / kQ4TParts, c1 = (part + 1) * chunks / kQ4TParts;
   if (threadIdx.x == 0) {
     for (int s = 0; s < L::kStages; ++s) {
@@ -167,6 +186,10 @@ __global__ void __launch_bounds__(Q4TLayout<NT>::kThreads)
   float acc[NT][4];
 #pragma unroll
   for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
+  // X is complete from here on, for the layer kernel too, which this lets start: it waits for
+  // this grid before it reads t
+  griddep_wait();
+  griddep_launch_dependents();
   if (warp == kQ4TWarps) {
     if (lane == 0) {
       int s = 0, ph = 0, issued = 0;
@@ -177,10 +200,11 @@ __global__ void __launch_bounds__(Q4TLayout<NT>::kThreads)
         }
         uint8_t* a = smem + s * L::kStage;
         uint64_t* bar = &ctrl->full[s];
-        mbar_arrive_expect_tx(bar, (R > 64 ? 16384 : 8192) + NT * 1024);
-        tma_load_2d(a, &ma, 0, c * 64, bar);
-        if (R > 64) tma_load_2d(a + 8192, &ma, 64, c * 64, bar);
-        tma_load_2d(a + 16384, &mx, c * 64, 0, bar);
+        // past K, both read as zero
+        mbar_arrive_expect_tx(bar, (R > 64 ? 32768 : 16384) + NT * 2048);
+        tma_load_2d(a, &ma, 0, c * 128, bar);
+        if (R > 64) tma_load_2d(a + 16384, &ma, 64, c * 128, bar);
+        tma_load_3d(a + 32768, &mx, 0, 0, 2 * c, bar);
         ++issued;
         if (++s == L::kStages) s = 0, ph ^= 1;
       }
@@ -198,10 +222,10 @@ __global__ void __launch_bounds__(Q4TLayout<NT>::kThreads)
       const uint8_t* tile = smem + s * L::kStage;
       if (live) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < 4; ++h) {
           uint32_t a[2][4];
-          q4_turned(smem_u32(tile) + (warp >> 2) * 8192, 32 * h, (warp & 3) * 2, lane, a);
-          const uint8_t* x = tile + 16384 + g * 128 + (((4 * h + tl) ^ g) << 4);
+          q4_turned(smem_u32(tile) + (warp >> 2) * 16384, 32 * h, (warp & 3) * 2, lane, a);
+          const uint8_t* x = tile + 32768 + (h >> 1) * NT * 1024 + g * 128 + (((4 * (h & 1) + tl) ^ g) << 4);
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             const uint4 v = *reinterpret_cast<const uint4*>(x + n * 1024);
@@ -256,13 +280,13 @@ __global__ void __launch_bounds__(Q4TLayout<NT>::kThreads)
 }
 
 // ------------------------------------------------------------------------------------
-// The layer for M <= 8 NT tokens.  Persistent CTAs, several to an SM: the weight's stages
-// (128 rows x 128 columns), row block by row block, are cut into one equal contiguous range
-// per CTA, so that every SM has the same work whatever the shape.  One producer thread
-// brings each stage's record by one bulk copy and its X tiles by TMA (128-byte swizzle;
-// tokens past M read as zero) into a ring; 8 / RT consumer warps, RT row tiles each, rebuild
-// the codes in registers and multiply.  The CTA whose range holds a row block's first stage
-// also takes the block's adapter, after its weight stages: 32 ranks a stage, B by TMA, read
+// The layer for M <= 8 NT tokens.  Persistent CTAs, several to an SM: the weight's records,
+// row block by row block, are cut into one equal contiguous range per CTA, so that every SM
+// has the same work whatever the shape.  One producer thread brings each stage (a record or
+// two) by one bulk copy and its X tiles by one TMA copy (128-byte swizzle; tokens past M
+// read as zero) into a ring; 8 / RT consumer warps, RT row tiles each, rebuild the codes in
+// registers and multiply.  The CTA whose range holds a row block's first record also takes
+// the block's adapter, after its weight stages: 32 ranks a stage, B by TMA, read
 // transposed, t in its two parts.  A block that lies in one range is written at once;
 // otherwise each warp stores its fp32 sums and the last one to arrive for a row tile adds
 // them up in the order of the ranges: results repeat bit for bit.
@@ -275,10 +299,13 @@ struct Q4Layout {
   static constexpr int kWarps = 8 / RT;
   static constexpr int kThreads = 32 * (kWarps + 1);
   static constexpr int kXHalf = NT * 1024;  // 8 NT tokens x 64 columns
-  static constexpr int kStage = 2 * kXHalf + 10240;
-  static constexpr int kStages = NT <= 2 ? 5 : 4;
+  // Records to a stage: with few tokens a record is so little work that the stage's
+  // handshake would take a third of the instructions.
+  static constexpr int kRecords = NT <= 2 ? 2 : 1;
+  static constexpr int kXBytes = 2 * kRecords * kXHalf;
+  static constexpr int kStage = kXBytes + (kRecords * kQ4MaxRecord + 1023) / 1024 * 1024;
+  static constexpr int kStages = NT <= 2 ? 3 : 4;
   static constexpr int kSmemBytes = kStages * kStage + 1024 + 256;
-  static_assert(kQ4MaxRecord <= 10240, "a record fits its stage");
   // CTAs per SM that the shared memory admits (1 KB of it is the system's, per CTA)
   static constexpr int kPerSm = 233472 / (kSmemBytes + 1024) > 4 ? 4 : 233472 / (kSmemBytes + 1024);
 };
@@ -290,19 +317,20 @@ struct Q4Params {
   uint32_t* count;  // [blocks][8 row tiles] arrivals, zero between calls
   int* status;
   int M, R;
-  int stages;       // of a row block
-  long long total;  // stages in all
+  int records;      // of a row block
+  long long total;  // records in all
 };
 
-// First stage of CTA c's range, of `ctas`; and the CTA whose range holds stage i.
+// First record of CTA c's range, of `ctas`; and the CTA whose range holds record i.
 __device__ __forceinline__ long long q4_range(long long total, int c, int ctas) { return total * c / ctas; }
 __device__ __forceinline__ int q4_owner(long long total, long long i, int ctas) {
   return static_cast<int>(((i + 1) * ctas - 1) / total);
 }
 
-// One stage of COLS columns of the weight into the sums.
+// A record of COLS columns into the sums.
 template <int NT, int GROUP, bool ZEROS, int COLS>
-__device__ __forceinline__ void q4_stage(const uint8_t* x, const uint8_t* rec, int warp, int lane,
+__device__ __forceinline__ void q4_record(const uint8_t* x, const uint8_t* rec, int warp, int lane,
+                                         uint32_t mask, uint32_t one28, uint32_t eight,
                                          float (&acc)[Q4Layout<NT>::RT][NT][4]) {
   using L = Q4Layout<NT>;
   constexpr int RT = L::RT;
@@ -326,7 +354,7 @@ __device__ __forceinline__ void q4_stage(const uint8_t* x, const uint8_t* rec, i
       uint32_t a[RT][2][4];
 #pragma unroll
       for (int r = 0; r < RT; ++r) {
-        uint32_t lo = 0x43084308u, hi = 0x43084308u;
+        uint32_t lo = eight, hi = eight;
         if (ZEROS) {
           const uint32_t z = *reinterpret_cast<const uint16_t*>(zeros + grp * 128 + r * 16);
           lo = q4_bias(z, 0);
@@ -338,22 +366,27 @@ __device__ __forceinline__ void q4_stage(const uint8_t* x, const uint8_t* rec, i
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             const int sh = 4 * (2 * i + j);
-            a[r][i][2 * j] = q4_sub2(((w0 >> sh) & 0x000f000fu) | 0x43004300u, lo);
-            a[r][i][2 * j + 1] = q4_sub2(((w1 >> sh) & 0x000f000fu) | 0x43004300u, hi);
+            a[r][i][2 * j] = q4_sub2(q4_pair(w0 >> sh, mask, one28), lo);
+            a[r][i][2 * j + 1] = q4_sub2(q4_pair(w1 >> sh, mask, one28), hi);
           }
       }
+      uint4 v[NT];
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const uint4 v = *reinterpret_cast<const uint4*>(xh[h] + b * L::kXHalf + n * 1024);
+      for (int n = 0; n < NT; ++n) v[n] = *reinterpret_cast<const uint4*>(xh[h] + b * L::kXHalf + n * 1024);
+      // all first products, then all second ones: neighbours do not wait for one another
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
           if (first)
-            mma_m16n8k16_zero(cc[r][n], a[r][0], v.x, v.y);
+            mma_m16n8k16_zero(cc[r][n], a[r][0], v[n].x, v[n].y);
           else
-            mma_m16n8k16(cc[r][n], a[r][0], v.x, v.y);
-          mma_m16n8k16(cc[r][n], a[r][1], v.z, v.w);
+            mma_m16n8k16(cc[r][n], a[r][0], v[n].x, v[n].y);
         }
-      }
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int r = 0; r < RT; ++r) mma_m16n8k16(cc[r][n], a[r][1], v[n].z, v[n].w);
       if (end) {
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
@@ -378,14 +411,15 @@ __global__ void __launch_bounds__(Q4Layout<NT>::kThreads, Q4Layout<NT>::kPerSm)
                      const __grid_constant__ CUtensorMap mt, const __grid_constant__ CUtensorMap mb) {
   using L = Q4Layout<NT>;
   constexpr int RT = L::RT;
+  constexpr int kRecord = 64 * kQ4Cols + kQ4Cols / GROUP * (ZEROS ? 384 : 256);  // bytes
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~static_cast<uintptr_t>(1023));
+  uint8_t* smem = align_1024(smem_raw);
   Q4Ctrl* ctrl = reinterpret_cast<Q4Ctrl*>(smem + L::kStages * L::kStage);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int cta = blockIdx.x, ctas = gridDim.x;
   const long long i0 = q4_range(p.total, cta, ctas), i1 = q4_range(p.total, cta + 1, ctas);
   const int ranks = (p.R + 31) / 32;  // adapter stages of a block
+  griddep_launch_dependents();  // a kernel launched to overlap this one waits for it itself
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < L::kStages; ++s) {
@@ -399,35 +433,50 @@ __global__ void __launch_bounds__(Q4Layout<NT>::kThreads, Q4Layout<NT>::kPerSm)
 
   if (warp == L::kWarps) {
     if (lane == 0) {
+      // a range's records lie one behind another: no addresses are computed per stage (their
+      // divisions and 64-bit products took this one thread longer than a stage's products)
+      const int first = static_cast<int>(i0 / p.records);
+      const uint8_t* rec = p.w.at(first, static_cast<int>(i0 - static_cast<long long>(first) * p.records));
+      const uint32_t tail = p.w.K % kQ4Cols ? p.w.record(p.w.K % kQ4Cols) : kRecord;
+      // The codes may come before the kernel ahead has completed; X (without adapters: after
+      // the t kernel has started, X is complete) and all that is written come after it.
+      const bool early = p.R == 0;
       int s = 0, ph = 0, issued = 0;
       bool ok = true, waited = false;
       for (long long i = i0; i < i1 && ok;) {
-        const int block = static_cast<int>(i / p.stages), c0 = static_cast<int>(i - static_cast<long long>(block) * p.stages);
-        const int n = static_cast<int>(min(static_cast<long long>(p.stages - c0), i1 - i));
-        const int extra = c0 == 0 ? ranks : 0;
-        for (int c = 0; c < n + extra; ++c) {
+        const int block = static_cast<int>(i / p.records), c0 = static_cast<int>(i - static_cast<long long>(block) * p.records);
+        const int n = static_cast<int>(min(static_cast<long long>(p.records - c0), i1 - i));
+        const int stages = (n + L::kRecords - 1) / L::kRecords, extra = c0 == 0 ? ranks : 0;
+        const int ahead = early && i == i0 ? min(stages, L::kStages) : 0;
+        for (int c = 0; c < stages + extra; ++c) {
           if (!mbar_wait(&ctrl->empty[s], ph ^ 1) || q4_aborted(ctrl)) {
             q4_abort(p.status, ctrl);
             ok = false;
             break;
           }
           uint8_t* x = smem + s * L::kStage;
-          uint8_t* rec = x + 2 * L::kXHalf;
+          uint8_t* dst = x + L::kXBytes;
           uint64_t* bar = &ctrl->full[s];
-          if (c < n) {
-            const int col = (c0 + c) * kQ4Cols, cols = min(kQ4Cols, p.w.K - col);
-            const uint32_t bytes = static_cast<uint32_t>(p.w.record(cols));
-            mbar_arrive_expect_tx(bar, bytes + cols / 64 * L::kXHalf);
-            bulk_g2s(rec, p.w.at(block, c0 + c), bytes, bar);
-            tma_load_2d(x, &mx, col, 0, bar);
-            if (cols > 64) tma_load_2d(x + L::kXHalf, &mx, col + 64, 0, bar);
+          if (c < stages) {
+            const int at = c0 + c * L::kRecords, cnt = min(L::kRecords, c0 + n - at);
+            // the last record of a block may be the shorter one
+            const uint32_t bytes = (cnt - 1) * kRecord + (at + cnt == p.records ? tail : kRecord);
+            mbar_arrive_expect_tx(bar, bytes + L::kXBytes);
+            bulk_g2s(dst, rec, bytes, bar);
+            if (c >= ahead) tma_load_3d(x, &mx, 0, 0, 2 * at, bar);
+            rec += bytes;
+            if (c + 1 == ahead) {  // every stage of the ring has its codes coming
+              griddep_wait();
+              for (int k = 0; k < ahead; ++k)
+                tma_load_3d(smem + k * L::kStage, &mx, 0, 0, 2 * (c0 + k * L::kRecords), &ctrl->full[k]);
+            }
           } else {
-            const int a = c - n;
+            const int a = c - stages;
             if (!waited) griddep_wait();  // t
             waited = true;
             mbar_arrive_expect_tx(bar, 8192 + L::kXHalf);
-            tma_load_2d(rec, &mb, block * 128, a * 32, bar);
-            tma_load_2d(rec + 4096, &mb, block * 128 + 64, a * 32, bar);
+            tma_load_2d(dst, &mb, block * 128, a * 32, bar);
+            tma_load_2d(dst + 4096, &mb, block * 128 + 64, a * 32, bar);
             tma_load_2d(x, &mt, a * 64, 0, bar);
           }
           ++issued;
@@ -444,29 +493,38 @@ __global__ void __launch_bounds__(Q4Layout<NT>::kThreads, Q4Layout<NT>::kPerSm)
   }
 
   const int g = lane >> 2, tl = lane & 3;
+  const uint32_t mask = q4_opaque(0x000f000fu), one28 = q4_opaque(0x43004300u), eight = q4_opaque(0x43084308u);
   int s = 0, ph = 0;
   for (long long i = i0; i < i1;) {
-    const int block = static_cast<int>(i / p.stages), c0 = static_cast<int>(i - static_cast<long long>(block) * p.stages);
-    const int n = static_cast<int>(min(static_cast<long long>(p.stages - c0), i1 - i));
-    const int extra = c0 == 0 ? ranks : 0;
+    const int block = static_cast<int>(i / p.records), c0 = static_cast<int>(i - static_cast<long long>(block) * p.records);
+    const int n = static_cast<int>(min(static_cast<long long>(p.records - c0), i1 - i));
+    const int stages = (n + L::kRecords - 1) / L::kRecords, extra = c0 == 0 ? ranks : 0;
     float acc[RT][NT][4];
 #pragma unroll
     for (int r = 0; r < RT; ++r)
 #pragma unroll
       for (int k = 0; k < NT; ++k) acc[r][k][0] = acc[r][k][1] = acc[r][k][2] = acc[r][k][3] = 0.f;
-    for (int c = 0; c < n + extra; ++c) {
+    // records of 128 columns yet to come in this segment; a shorter one ends the block
+    int wide = c0 + n == p.records && p.w.K % kQ4Cols ? n - 1 : n;
+    const bool narrow = wide < n;
+    for (int c = 0; c < stages + extra; ++c) {
       const bool ok = mbar_wait(&ctrl->full[s], ph);
       if (!__all_sync(0xffffffffu, ok)) {
         q4_abort(p.status, ctrl);
         return;
       }
       const uint8_t* x = smem + s * L::kStage;
-      const uint8_t* rec = x + 2 * L::kXHalf;
-      if (c < n) {
-        if (GROUP == 128 || p.w.K - (c0 + c) * kQ4Cols >= kQ4Cols)
-          q4_stage<NT, GROUP, ZEROS, kQ4Cols>(x, rec, warp, lane, acc);
-        else
-          q4_stage<NT, GROUP, ZEROS, GROUP == 128 ? 128 : 64>(x, rec, warp, lane, acc);
+      const uint8_t* rec = x + L::kXBytes;
+      if (c < stages) {
+#pragma unroll
+        for (int k = 0; k < L::kRecords; ++k, --wide) {
+          if (wide > 0)
+            q4_record<NT, GROUP, ZEROS, kQ4Cols>(x + k * 2 * L::kXHalf, rec + k * kRecord, warp, lane, mask, one28,
+                                                 eight, acc);
+          else if (GROUP < 128 && narrow && wide == 0)
+            q4_record<NT, GROUP, ZEROS, GROUP == 128 ? 128 : 64>(x + k * 2 * L::kXHalf, rec + k * kRecord, warp,
+                                                                 lane, mask, one28, eight, acc);
+        }
       } else {
         uint32_t a[RT][2][4];
 #pragma unroll
@@ -493,7 +551,8 @@ __global__ void __launch_bounds__(Q4Layout<NT>::kThreads, Q4Layout<NT>::kPerSm)
     if (q4_aborted(ctrl)) return;  // the values are not whole: nothing of the block is written
     // this warp's rows of the block: values (row, token) at 4 places of each 16 x 8 tile
     const size_t n0 = static_cast<size_t>(block) * 128;
-    auto each = [&](auto&& f) {
+    int place = 0;
+    auto each = [&](auto&& f, int& j) {
 #pragma unroll
       for (int r = 0; r < RT; ++r)
 #pragma unroll
@@ -501,35 +560,51 @@ __global__ void __launch_bounds__(Q4Layout<NT>::kThreads, Q4Layout<NT>::kPerSm)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int m = 8 * k + 2 * tl + (e & 1), row = (warp * RT + r) * 16 + g + 8 * (e >> 1);
+            j = (r * NT + k) * 4 + e;
             if (m < p.M) f(acc[r][k][e], m, row);
           }
     };
     auto store = [&](float v, int m, int row) {
       reinterpret_cast<__nv_bfloat16*>(p.Y)[static_cast<size_t>(m) * p.w.N + n0 + row] = __float2bfloat16_rn(v);
     };
-    if (n == p.stages) {
-      each(store);
+    if (n == p.records) {
+      each(store, place);
     } else {
       const size_t slot = static_cast<size_t>(p.M) * 128;
       // a block that the range starts in takes the CTA's slot 0, one that it ends in slot 1
       float* mine = p.part + (2 * static_cast<size_t>(cta) + (i == i0 ? 0 : 1)) * slot;
-      each([&](float v, int m, int row) { __stcg(mine + m * 128 + row, v); });
+      each([&](float v, int m, int row) { __stcg(mine + m * 128 + row, v); }, place);
       __threadfence();
       __syncwarp();
-      const long long b0 = static_cast<long long>(block) * p.stages;
-      const int f = q4_owner(p.total, b0, ctas), l = q4_owner(p.total, b0 + p.stages - 1, ctas);
+      const long long b0 = static_cast<long long>(block) * p.records;
+      const int f = q4_owner(p.total, b0, ctas), l = q4_owner(p.total, b0 + p.records - 1, ctas);
       uint32_t last = 0;
       if (lane == 0) last = atomicAdd(p.count + block * 8 + warp, 1u) == static_cast<uint32_t>(l - f);
       if (__shfl_sync(0xffffffffu, last, 0)) {
         __threadfence();
         // the first CTA of the block has it in slot 1 unless its range starts with the block
         const float* from = p.part + (2 * static_cast<size_t>(f) + (q4_range(p.total, f, ctas) == b0 ? 0 : 1)) * slot;
-        each([&](float& v, int m, int row) { v = __ldcg(from + m * 128 + row); });
-        for (int c = f + 1; c <= l; ++c) {
-          const float* next = p.part + 2 * static_cast<size_t>(c) * slot;
-          each([&](float& v, int m, int row) { v += __ldcg(next + m * 128 + row); });
+        each([&](float& v, int m, int row) { v = __ldcg(from + m * 128 + row); }, place);
+        const float* next = p.part + 2 * static_cast<size_t>(f + 1) * slot;
+        int c = f + 1;
+        // the values of several ranges at once: one trip to L2 for all of them
+        constexpr int kAtOnce = NT <= 2 ? 4 : 1;
+        for (; c + kAtOnce <= l + 1; c += kAtOnce, next += 2 * kAtOnce * slot) {
+          float v[kAtOnce][RT * NT * 4];
+#pragma unroll
+          for (int k = 0; k < kAtOnce; ++k) {
+            int j = 0;
+            each([&](float&, int m, int row) { v[k][j] = __ldcg(next + 2 * k * slot + m * 128 + row); }, j);
+          }
+#pragma unroll
+          for (int k = 0; k < kAtOnce; ++k) {
+            int j = 0;
+            each([&](float& a, int, int) { a += v[k][j]; }, j);
+          }
         }
-        each(store);
+        for (; c <= l; ++c, next += 2 * slot)
+          each([&](float& v, int m, int row) { v += __ldcg(next + m * 128 + row); }, place);
+        each(store, place);
         if (lane == 0) p.count[block * 8 + warp] = 0u;
       }
     }
