@@ -6,6 +6,7 @@ passed as raw pointers to their 16-bit patterns.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -109,13 +110,27 @@ def _check(fn: str, code: int):
 
 
 def _stream_ptr(stream=None):
+    """The stream's handle; by default the current stream of the current device (looked up
+    without building a Stream object, which takes longer than queueing a kernel)."""
+    if stream is not None:
+        return stream.cuda_stream
     import torch
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+
+
+def _on_device(t):
+    """Context in which the device of CUDA tensor ``t`` is the current one."""
+    import torch
+    if t.get_device() == torch._C._cuda_getDevice():
+        return _HERE
+    return torch.cuda.device(t.device)
+
+
+_HERE = contextlib.nullcontext()
 
 
 def _ptr(t):
-    return ctypes.c_void_p(t.data_ptr()) if t is not None else ctypes.c_void_p(0)
+    return t.data_ptr() if t is not None else 0
 
 
 def _require(t, name, shape=None, device=True):
@@ -249,7 +264,7 @@ def pack_q4(codes, scales, zeros=None, stream=None) -> Weight:
     if not scales.shape[1] or K % scales.shape[1]:
         raise ValueError("scales must have one column per group of equal size")
     h = _P()
-    with torch.cuda.device(codes.device):
+    with _on_device(codes):
         _check("salr_q4_pack", load_library().salr_q4_pack(
             _ptr(codes), _ptr(scales), _ptr(zeros), N, K, K // scales.shape[1],
             _stream_ptr(stream), ctypes.byref(h)))
@@ -259,11 +274,10 @@ def pack_q4(codes, scales, zeros=None, stream=None) -> Weight:
 def encode_q4(W, group: int = 64, symmetric: bool = True, stream=None) -> Weight:
     """salr_q4_encode: round ``W`` (N x K bf16, CUDA) to 4-bit codes with a bf16 scale, and a
     zero point unless ``symmetric``, per ``group`` columns of a row."""
-    import torch
     _require(W, "W")
     N, K = W.shape
     h = _P()
-    with torch.cuda.device(W.device):
+    with _on_device(W):
         _check("salr_q4_encode", load_library().salr_q4_encode(
             _ptr(W), N, K, int(group), 1 if symmetric else 0, _stream_ptr(stream),
             ctypes.byref(h)))
@@ -308,7 +322,6 @@ def residual_adapter(W, weight: Weight, r: int, q: int = 2, oversample: int = 16
 
 def linear(X, weight: Weight, A_cat=None, B_cat=None, Y=None, stream=None):
     """salr_linear: Y = X (M.W)^T + (X A_cat) B_cat; returns Y (M x N bf16)."""
-    import torch
     N, K = weight._shape()
     _require(X, "X")
     M = X.shape[0]
@@ -320,7 +333,7 @@ def linear(X, weight: Weight, A_cat=None, B_cat=None, Y=None, stream=None):
         _require(A_cat, "A_cat", (K, R))
         _require(B_cat, "B_cat", (R, N))
     if Y is None:
-        Y = torch.empty(M, N, dtype=torch.bfloat16, device=X.device)
+        Y = X.new_empty((M, N))
     else:
         _require(Y, "Y", (M, N))
     _check("salr_linear", load_library().salr_linear(_ptr(X), M, weight.handle, _ptr(A_cat),
@@ -333,7 +346,6 @@ def linear_backward(dY, X, weight: Weight, A_cat=None, B_cat=None, dX=None, dA=N
     """salr_linear_backward: the gradients (dX, dA, dB) of ``linear`` for the gradient ``dY``
     of its result (M x N bf16).  ``needs`` says which are wanted; the others, and dA and dB
     without adapters, come back as None.  ``X`` may be None if only dX is wanted."""
-    import torch
     N, K = weight._shape()
     _require(dY, "dY")
     if dY.dim() != 2 or dY.shape[1] != N:
@@ -357,12 +369,12 @@ def linear_backward(dY, X, weight: Weight, A_cat=None, B_cat=None, dX=None, dA=N
         if not want:
             t = None
         elif t is None:
-            t = torch.empty(shape, dtype=torch.bfloat16, device=dY.device)
+            t = dY.new_empty(shape)
         else:
             _require(t, name, shape)
         out.append(t)
     dX, dA, dB = out
-    with torch.cuda.device(dY.device):
+    with _on_device(dY):
         _check("salr_linear_backward", load_library().salr_linear_backward(
             _ptr(dY), _ptr(X), M, weight.handle, _ptr(A_cat), _ptr(B_cat), R, _ptr(dX), _ptr(dA),
             _ptr(dB), _stream_ptr(stream)))

@@ -9,7 +9,9 @@ from __future__ import annotations
 import ctypes
 import math
 
-from .binding import AdamwConfig, AdamwTensor, _check, _stream_ptr, load_library
+import numpy as np
+
+from .binding import AdamwConfig, AdamwTensor, _check, _on_device, _stream_ptr, load_library
 
 BLOCK = 256  # elements that share a scale of the 8-bit moments
 _TYPES = {"torch.bfloat16": 0, "torch.float32": 1}
@@ -99,6 +101,10 @@ class AdamW:
             if master:
                 t.master = self.master.data_ptr() + s.start * 4
             t.n = p.numel()
+        # the gradients' pointers in the table, as one strided array
+        self._grads = np.frombuffer(self._table, dtype=np.uint64).reshape(len(self._table), -1)[
+            :, AdamwTensor.grad.offset // 8]
+        self._index = self._step.get_device()
         self._config = AdamwConfig(beta1=beta1, beta2=beta2, eps=eps, step=self._step.data_ptr(),
                                    param_type=_TYPES[str(first.dtype)], state_bits=state_bits,
                                    master=1 if master else 0)
@@ -117,24 +123,29 @@ class AdamW:
         ``grad_scale``: a one-element float32 CUDA tensor that multiplies every gradient (the
         factor of gradient clipping, or of undoing a loss scale)."""
         import torch
+        T = torch.Tensor
         if len(grads) != len(self.params):
             raise ValueError(f"{len(grads)} gradients for {len(self.params)} params")
-        kind = None
-        device, table = self.device, self._table
-        for i, g in enumerate(grads):
-            if g is None:
-                table[i].grad = None
-                continue
-            if kind is None:
-                kind = g.dtype
-                if str(kind) not in _TYPES:
-                    raise TypeError("grads must be bfloat16 or float32")
-            if g.dtype != kind:
-                raise TypeError("grads must have one type")
-            if g.numel() != self._numel[i] or not g.is_contiguous() or g.device != device:
-                raise ValueError(f"grads[{i}] must be contiguous, as large as its parameter and "
-                                 f"on {device}")
-            table[i].grad = g.data_ptr()
+        if type(grads) is not list:
+            grads = list(grads)
+        # whole-list passes: a loop over hundreds of gradients would take longer than the step
+        given = grads
+        try:
+            pointers = list(map(T.data_ptr, grads))
+            numel = self._numel
+        except TypeError:  # None among them
+            given = [g for g in grads if g is not None]
+            pointers = [0 if g is None else g.data_ptr() for g in grads]
+            numel = [n for n, g in zip(self._numel, grads) if g is not None]
+        kinds = set(map(T.dtype.__get__, given))
+        kind = kinds.pop() if kinds else None
+        if kinds or (kind is not None and str(kind) not in _TYPES):
+            raise TypeError("grads must have one type, bfloat16 or float32")
+        if (list(map(T.numel, given)) != numel or not all(map(T.is_contiguous, given)) or
+                any(i != self._index for i in set(map(T.get_device, given)))):
+            raise ValueError(f"each gradient must be contiguous, as large as its parameter and "
+                             f"on {self.device}")
+        self._grads[:] = pointers
         c = self._config
         c.grad_type = 0 if kind is None else _TYPES[str(kind)]
         c.lr, c.lr_dev = 0.0, None
@@ -146,6 +157,6 @@ class AdamW:
             c.lr = lr
         c.weight_decay = self.weight_decay
         c.grad_scale = None if grad_scale is None else self._scalar(grad_scale, "grad_scale")
-        with torch.cuda.device(device):
-            _check("salr_adamw", load_library().salr_adamw(table, len(table), ctypes.byref(c),
+        with _on_device(self._step):
+            _check("salr_adamw", load_library().salr_adamw(self._table, len(self._table), ctypes.byref(c),
                                                            _stream_ptr(stream)))
