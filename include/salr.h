@@ -422,7 +422,8 @@ SALR_API int salr_linear_backward(const void* dY, const void* X, int64_t M, salr
  *     m  = beta1 m + (1 - beta1) g'         v = beta2 v + (1 - beta2) g'^2
  *     p  = (1 - lr weight_decay) p - lr / (1 - beta1^t) m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
  *
- * in fp32, each operation rounded to nearest on its own.  The step advances step[0] by one.
+ * in fp32, each operation rounded to nearest on its own, but sqrt(v) within 2^-23 and the
+ * quotient m / (...) within 2 units in the last place.  The step advances step[0] by one.
  *
  * tensors  host array of `count` entries, read before the call returns.  An entry with
  *          n == 0 or grad == NULL is skipped (its moments stay as they are; the one step

@@ -4,7 +4,8 @@
 //   m <- b1 m + (1 - b1) g'          v <- b2 v + (1 - b2) g'^2
 //   p <- (1 - lr wd) p - lr / (1 - b1^t) * m / (sqrt(v) / sqrt(1 - b2^t) + eps)
 // Every fp32 operation is rounded on its own (no contraction into fused multiply-adds), so
-// that the 8-bit codes below do not depend on how a compiler groups the operations.
+// that the 8-bit codes below do not depend on how a compiler groups the operations; the
+// square root is within 2^-23 and the quotient within 2 units in the last place.
 //
 // 8-bit moments: blocks of 256 consecutive elements of a tensor hold m and r = sqrt(v) as
 // e4m3 values x / scale with one fp32 scale = max|x| / 448 per block.  r rather than v: its
@@ -29,6 +30,7 @@ namespace salr {
 constexpr int kAdamBlock = 256;    // elements per warp pass and per 8-bit scale
 constexpr int kAdamThreads = 256;  // 8 warps
 constexpr float kE4m3Max = 448.f;
+constexpr float kE4m3Tiny = 0.001953125f;               // 2^-9, the smallest positive value
 constexpr float kAdamFlush = 7.888609052210118e-31f;  // 2^-100
 
 struct AdamTensor {  // as salr_adamw_tensor
@@ -65,6 +67,13 @@ __device__ __forceinline__ double adam_pow(double b, long long t) {
   for (; t > 0; t >>= 1, b *= b)
     if (t & 1) r *= b;
   return r;
+}
+
+// Square root to 2^-23 (the fully rounded one takes a branch and three times the instructions).
+__device__ __forceinline__ float adam_sqrt(float x) {
+  float d;
+  asm("sqrt.approx.f32 %0, %1;" : "=f"(d) : "f"(x));
+  return d;
 }
 
 // 8 consecutive values at element i of p, as fp32 (p + i is 16-byte aligned).
@@ -122,11 +131,6 @@ __device__ __forceinline__ void adam_put(T* p, int64_t i, int cnt, bool vec, con
   }
 }
 
-__device__ __forceinline__ float e4m3_value(uint32_t code) {
-  const __half_raw h = __nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(code), __NV_E4M3);
-  return __half2float(__half(h));
-}
-
 // The thread's 8 codes at element i.  Codes start 8-byte aligned in every tensor, and the
 // caller pads a tensor's codes to whole blocks.
 __device__ __forceinline__ uint2 adam_codes(const void* p, int64_t i) {
@@ -134,8 +138,24 @@ __device__ __forceinline__ uint2 adam_codes(const void* p, int64_t i) {
 }
 __device__ __forceinline__ void adam_decode(uint2 c, float scale, float (&x)[8]) {
 #pragma unroll
-  for (int k = 0; k < 8; ++k)
-    x[k] = __fmul_rn(e4m3_value(((k < 4 ? c.x : c.y) >> (8 * (k & 3))) & 255u), scale);
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t w = (k < 2 ? c.x : c.y) >> (16 * (k & 1));
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w), __NV_E4M3);
+    const float2 f = __half22float2(__half2(h));
+    x[2 * k] = __fmul_rn(f.x, scale);
+    x[2 * k + 1] = __fmul_rn(f.y, scale);
+  }
+}
+__device__ __forceinline__ uint32_t adam_e4m3x4(float a, float b, float c, float d) {
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+  return lo | hi << 16;
+}
+// The larger value, or NaN if either is.
+__device__ __forceinline__ float adam_max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
 }
 
 // Store x (8 values a thread, the warp's block) as e4m3 codes at element i and the block's
@@ -143,26 +163,45 @@ __device__ __forceinline__ void adam_decode(uint2 c, float scale, float (&x)[8])
 template <bool POSITIVE>
 __device__ __forceinline__ void adam_encode(const float (&x)[8], void* codes, int64_t i, float* sp,
                                             int lane) {
-  float top = 0.f;
+  constexpr float kMax = 3.402823466e38f;
+  float top = fabsf(x[0]);
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const float a = fabsf(x[k]);
-    top = a <= 3.402823466e38f ? fmaxf(top, a) : top;  // finite values only
+  for (int k = 1; k < 8; ++k) top = adam_max_nan(top, fabsf(x[k]));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = adam_max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const bool finite = top <= kMax;  // the same in every lane
+  if (!finite) {                    // the largest finite value instead
+    top = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (fabsf(x[k]) <= kMax) top = fmaxf(top, fabsf(x[k]));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   const bool live = top >= kAdamFlush;
   const float inv = live ? __fdiv_rn(kE4m3Max, top) : 0.f;
-  uint32_t w[2] = {0, 0};
+  float y[8];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const float y = __fmul_rn(x[k], inv);
-    uint32_t c = __nv_cvt_float_to_fp8(y, __NV_SATFINITE, __NV_E4M3);
-    if (POSITIVE && y > 0.f && c == 0) c = 1;
-    if (!(fabsf(x[k]) <= 3.402823466e38f)) c = 0x7f;  // NaN
-    w[k >> 2] |= c << (8 * (k & 3));
+  for (int k = 0; k < 8; ++k) y[k] = __fmul_rn(x[k], inv);
+  if (POSITIVE && live) {  // what is above zero stays so
+    float low = x[0];
+#pragma unroll
+    for (int k = 1; k < 8; ++k) low = fminf(low, x[k]);
+    if (low > 0.f) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) y[k] = fmaxf(y[k], kE4m3Tiny);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) y[k] = x[k] > 0.f ? fmaxf(y[k], kE4m3Tiny) : y[k];
+    }
   }
-  __stcs(reinterpret_cast<uint2*>(static_cast<uint8_t*>(codes) + i), make_uint2(w[0], w[1]));
+  if (!finite) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (!(fabsf(x[k]) <= kMax)) y[k] = __int_as_float(0x7fffffff);  // NaN is held as NaN
+  }
+  __stcs(reinterpret_cast<uint2*>(static_cast<uint8_t*>(codes) + i),
+         make_uint2(adam_e4m3x4(y[0], y[1], y[2], y[3]), adam_e4m3x4(y[4], y[5], y[6], y[7])));
   if (lane == 0) *sp = live ? __fdiv_rn(top, kE4m3Max) : 0.f;
 }
 
@@ -172,7 +211,6 @@ __global__ void __launch_bounds__(kAdamThreads)
   __shared__ float sh[4];
   const int lane = threadIdx.x & 31;
   const int total = tab.start[tab.count];
-  const int warps = gridDim.x * (kAdamThreads / 32);
   long long t = 0;
   if (threadIdx.x == 0) {
     t = tab.s.step[0] + 1;
@@ -186,14 +224,22 @@ __global__ void __launch_bounds__(kAdamThreads)
   const float rate = sh[0], root = sh[1], decay = sh[2], gscale = sh[3];
   const float eps = tab.s.eps, b1 = tab.s.b1, ob1 = tab.s.ob1, b2 = tab.s.b2, ob2 = tab.s.ob2;
 
-  for (int b = blockIdx.x * (kAdamThreads / 32) + (threadIdx.x >> 5); b < total; b += warps) {
-    int lo = 0, hi = tab.count;  // start[lo] <= b < start[hi]
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (tab.start[mid] <= b)
-        lo = mid;
-      else
-        hi = mid;
+  // A CTA takes a contiguous range of blocks, so that its warps look a tensor up only where
+  // one ends (a search for every block took 7 of some 100 instructions per 8-bit element).
+  const int first = static_cast<int>(static_cast<int64_t>(blockIdx.x) * total / gridDim.x);
+  const int behind = static_cast<int>(static_cast<int64_t>(blockIdx.x + 1) * total / gridDim.x);
+  int lo = 0, end = 0;  // the tensor of block b, and the block behind it
+  for (int b = first + (threadIdx.x >> 5); b < behind; b += kAdamThreads / 32) {
+    if (b >= end) {
+      int hi = tab.count;  // start[lo] <= b < start[hi]
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (tab.start[mid] <= b)
+          lo = mid;
+        else
+          hi = mid;
+      }
+      end = tab.start[lo + 1];
     }
     const AdamTensor& e = tab.t[lo];
     const int64_t blk = b - tab.start[lo];
@@ -230,14 +276,16 @@ __global__ void __launch_bounds__(kAdamThreads)
       if (EIGHT) v[k] = __fmul_rn(v[k], v[k]);
       m[k] = __fadd_rn(__fmul_rn(m[k], b1), __fmul_rn(gk, ob1));
       v[k] = __fadd_rn(__fmul_rn(v[k], b2), __fmul_rn(__fmul_rn(gk, gk), ob2));
-      r[k] = __fsqrt_rn(v[k]);
-      const float step = __fdiv_rn(m[k], __fadd_rn(__fmul_rn(r[k], root), eps));
+      r[k] = adam_sqrt(v[k]);
+      const float step = __fdividef(m[k], __fadd_rn(__fmul_rn(r[k], root), eps));
       p[k] = __fsub_rn(__fmul_rn(p[k], decay), __fmul_rn(rate, step));
     }
     if (EIGHT) {
+      if (cnt < 8) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (k >= cnt) m[k] = r[k] = 0.f;  // past the tensor's end (codes there are padding)
+        for (int k = 0; k < 8; ++k)
+          if (k >= cnt) m[k] = r[k] = 0.f;  // past the tensor's end (codes there are padding)
+      }
       adam_encode<false>(m, e.m, i, e.m_scale + blk, lane);
       adam_encode<true>(r, e.v, i, e.v_scale + blk, lane);
     } else {
