@@ -28,8 +28,10 @@ int launch(const AdamTable<MAXT>& tab, int dev, cudaStream_t st) {
     SALR_TRY(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, kAdamThreads, 0));
     resident[dev] = n > 0 ? n : 1;
   }
-  const int ctas = (tab.start[tab.count] + kAdamThreads / 32 - 1) / (kAdamThreads / 32);
-  const int grid = std::max(1, std::min(ctas, device_sms(dev) * resident[dev].load()));
+  // One block a warp while all CTAs are resident; then up to four times as many CTAs as are,
+  // of 64 blocks or more, so that the SMs even out at the end.
+  const int total = tab.start[tab.count], slots = device_sms(dev) * resident[dev].load();
+  const int grid = std::max(1, std::min((total + 7) / 8, std::max(slots, std::min(4 * slots, total / 64))));
   kern<<<grid, kAdamThreads, 0, st>>>(tab);
   SALR_TRY(cudaGetLastError());
   return SALR_OK;

@@ -17,13 +17,15 @@
 //
 // Bound: HBM.  An element moves 28 bytes with bf16 parameters and gradients, fp32 moments
 // and master copies, and 10 bytes with 8-bit moments and no master copies, so the work is
-// laid out for loads in flight: one warp per 256-element block, 8 elements a thread, every
-// load of a block issued before the first use (up to 112 bytes a thread).  The tensor
+// laid out for loads in flight: one warp per 256-element block, 8 elements a thread, the next
+// block's loads (up to 96 bytes a thread) issued before this one is worked on.  The tensor
 // table travels in the kernel's parameters: no copy, nothing to keep alive, one launch.
 #pragma once
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
+
+#include <type_traits>
 
 namespace salr {
 
@@ -76,58 +78,82 @@ __device__ __forceinline__ float adam_sqrt(float x) {
   return d;
 }
 
-// 8 consecutive values at element i of p, as fp32 (p + i is 16-byte aligned).
-__device__ __forceinline__ void adam_load8(const float* p, int64_t i, float (&x)[8]) {
-  const float4 a = __ldcs(reinterpret_cast<const float4*>(p + i));
-  const float4 b = __ldcs(reinterpret_cast<const float4*>(p + i) + 1);
-  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-  x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-}
-__device__ __forceinline__ void adam_load8(const __nv_bfloat16* p, int64_t i, float (&x)[8]) {
-  const uint4 a = __ldcs(reinterpret_cast<const uint4*>(p + i));
-  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    x[2 * k] = __uint_as_float(w[k] << 16);
-    x[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+// 8 values as they lie in memory, loaded ahead of their use.
+template <typename T>
+struct AdamRaw;
+template <>
+struct AdamRaw<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = __ldcs(reinterpret_cast<const float4*>(p));
+    b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
   }
+  __device__ __forceinline__ void load(const float* p, int cnt) {  // the first cnt; the rest 0
+    float x[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[k] = k < cnt ? p[k] : 0.f;
+    a = make_float4(x[0], x[1], x[2], x[3]);
+    b = make_float4(x[4], x[5], x[6], x[7]);
+  }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+    x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+  }
+};
+template <>
+struct AdamRaw<__nv_bfloat16> {
+  uint4 a;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { a = __ldcs(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ void load(const __nv_bfloat16* p, int cnt) {
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint16_t* q = reinterpret_cast<const uint16_t*>(p) + 2 * k;
+      w[k] = (2 * k < cnt ? q[0] : 0u) | (2 * k + 1 < cnt ? static_cast<uint32_t>(q[1]) << 16 : 0u);
+    }
+    a = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      x[2 * k] = __uint_as_float(w[k] << 16);
+      x[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+    }
+  }
+};
+__device__ __forceinline__ void adam_store8(float* p, const float (&x)[8]) {
+  __stcs(reinterpret_cast<float4*>(p), make_float4(x[0], x[1], x[2], x[3]));
+  __stcs(reinterpret_cast<float4*>(p) + 1, make_float4(x[4], x[5], x[6], x[7]));
 }
-__device__ __forceinline__ void adam_store8(float* p, int64_t i, const float (&x)[8]) {
-  __stcs(reinterpret_cast<float4*>(p + i), make_float4(x[0], x[1], x[2], x[3]));
-  __stcs(reinterpret_cast<float4*>(p + i) + 1, make_float4(x[4], x[5], x[6], x[7]));
-}
-__device__ __forceinline__ void adam_store8(__nv_bfloat16* p, int64_t i, const float (&x)[8]) {
+__device__ __forceinline__ void adam_store8(__nv_bfloat16* p, const float (&x)[8]) {
   uint32_t w[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * k], x[2 * k + 1]);
     w[k] = *reinterpret_cast<const uint32_t*>(&h);
   }
-  __stcs(reinterpret_cast<uint4*>(p + i), make_uint4(w[0], w[1], w[2], w[3]));
+  __stcs(reinterpret_cast<uint4*>(p), make_uint4(w[0], w[1], w[2], w[3]));
 }
-__device__ __forceinline__ float adam_float(float x) { return x; }
-__device__ __forceinline__ float adam_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ void adam_set(float* p, float x) { *p = x; }
 __device__ __forceinline__ void adam_set(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 
-// The `cnt` (1 .. 8) values from element i on, by vectors where allowed; the rest are 0.
+// The `cnt` (0 .. 8) values from p on, by vectors where allowed.
 template <typename T>
-__device__ __forceinline__ void adam_get(const T* p, int64_t i, int cnt, bool vec, float (&x)[8]) {
-  if (vec && cnt == 8) {
-    adam_load8(p, i, x);
-  } else {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) x[k] = k < cnt ? adam_float(p[i + k]) : 0.f;
-  }
+__device__ __forceinline__ void adam_get(AdamRaw<T>& r, const T* p, int cnt, bool vec) {
+  if (vec && cnt == 8)
+    r.load(p);
+  else
+    r.load(p, cnt);
 }
 template <typename T>
-__device__ __forceinline__ void adam_put(T* p, int64_t i, int cnt, bool vec, const float (&x)[8]) {
+__device__ __forceinline__ void adam_put(T* p, int cnt, bool vec, const float (&x)[8]) {
   if (vec && cnt == 8) {
-    adam_store8(p, i, x);
+    adam_store8(p, x);
   } else {
 #pragma unroll
     for (int k = 0; k < 8; ++k)
-      if (k < cnt) adam_set(p + i + k, x[k]);
+      if (k < cnt) adam_set(p + k, x[k]);
   }
 }
 
@@ -158,6 +184,17 @@ __device__ __forceinline__ float adam_max_nan(float a, float b) {
   return d;
 }
 
+__device__ __forceinline__ float adam_warp_max_nan(float a) {
+  float d;
+  asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(d) : "f"(a));
+  return d;
+}
+__device__ __forceinline__ float adam_rcp(float x) {  // within 2^-23
+  float d;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(d) : "f"(x));
+  return d;
+}
+
 // Store x (8 values a thread, the warp's block) as e4m3 codes at element i and the block's
 // scale at *sp.  All 32 lanes call it together.
 template <bool POSITIVE>
@@ -167,19 +204,19 @@ __device__ __forceinline__ void adam_encode(const float (&x)[8], void* codes, in
   float top = fabsf(x[0]);
 #pragma unroll
   for (int k = 1; k < 8; ++k) top = adam_max_nan(top, fabsf(x[k]));
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = adam_max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
-  const bool finite = top <= kMax;  // the same in every lane
-  if (!finite) {                    // the largest finite value instead
+  top = adam_warp_max_nan(top);
+  const bool plain = top <= 1e37f;  // the same in every lane
+  float inv = kE4m3Max * adam_rcp(top);
+  if (!plain) {  // infinite or NaN, of which the largest finite value counts, or near overflow
     top = 0.f;
 #pragma unroll
     for (int k = 0; k < 8; ++k)
       if (fabsf(x[k]) <= kMax) top = fmaxf(top, fabsf(x[k]));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    top = adam_warp_max_nan(top);
+    inv = __fdiv_rn(kE4m3Max, top);
   }
   const bool live = top >= kAdamFlush;
-  const float inv = live ? __fdiv_rn(kE4m3Max, top) : 0.f;
+  if (!live) inv = 0.f;
   float y[8];
 #pragma unroll
   for (int k = 0; k < 8; ++k) y[k] = __fmul_rn(x[k], inv);
@@ -195,18 +232,18 @@ __device__ __forceinline__ void adam_encode(const float (&x)[8], void* codes, in
       for (int k = 0; k < 8; ++k) y[k] = x[k] > 0.f ? fmaxf(y[k], kE4m3Tiny) : y[k];
     }
   }
-  if (!finite) {
+  if (!plain) {
 #pragma unroll
     for (int k = 0; k < 8; ++k)
       if (!(fabsf(x[k]) <= kMax)) y[k] = __int_as_float(0x7fffffff);  // NaN is held as NaN
   }
   __stcs(reinterpret_cast<uint2*>(static_cast<uint8_t*>(codes) + i),
          make_uint2(adam_e4m3x4(y[0], y[1], y[2], y[3]), adam_e4m3x4(y[4], y[5], y[6], y[7])));
-  if (lane == 0) *sp = live ? __fdiv_rn(top, kE4m3Max) : 0.f;
+  if (lane == 0) *sp = live ? top * (1.f / kE4m3Max) : 0.f;
 }
 
 template <int MAXT, typename PT, typename GT, bool MASTER, bool EIGHT>
-__global__ void __launch_bounds__(kAdamThreads)
+__global__ void __launch_bounds__(kAdamThreads, EIGHT ? 4 : 3)
     salr_adamw_kernel(const __grid_constant__ AdamTable<MAXT> tab) {
   __shared__ float sh[4];
   const int lane = threadIdx.x & 31;
@@ -228,8 +265,24 @@ __global__ void __launch_bounds__(kAdamThreads)
   // one ends (a search for every block took 7 of some 100 instructions per 8-bit element).
   const int first = static_cast<int>(static_cast<int64_t>(blockIdx.x) * total / gridDim.x);
   const int behind = static_cast<int>(static_cast<int64_t>(blockIdx.x + 1) * total / gridDim.x);
-  int lo = 0, end = 0;  // the tensor of block b, and the block behind it
-  for (int b = first + (threadIdx.x >> 5); b < behind; b += kAdamThreads / 32) {
+  // One block of this warp as loaded; the next one's loads go out before it is worked on.
+  struct Loaded {
+    int tensor;
+    int64_t blk;
+    AdamRaw<GT> g;
+    AdamRaw<typename std::conditional<MASTER, float, PT>::type> p;
+    AdamRaw<float> m, v;
+    uint2 mc, vc;
+    float ms, vs;
+  };
+  int lo = 0, end = 0;  // the tensor of the block loaded last, and the block behind it
+  auto place = [&](const AdamTensor& e, int64_t blk, int64_t& i, int& cnt, bool& vec) {
+    i = blk * kAdamBlock + lane * 8;
+    const int64_t left = e.n - i;
+    cnt = left >= 8 ? 8 : left > 0 ? static_cast<int>(left) : 0;
+    vec = ((reinterpret_cast<uintptr_t>(e.param) | reinterpret_cast<uintptr_t>(e.grad)) & 15) == 0;
+  };
+  auto load = [&](int b, Loaded& d) {
     if (b >= end) {
       int hi = tab.count;  // start[lo] <= b < start[hi]
       while (hi - lo > 1) {
@@ -242,34 +295,43 @@ __global__ void __launch_bounds__(kAdamThreads)
       end = tab.start[lo + 1];
     }
     const AdamTensor& e = tab.t[lo];
-    const int64_t blk = b - tab.start[lo];
-    const int64_t i = blk * kAdamBlock + lane * 8;
-    const int64_t left = e.n - i;
-    const int cnt = left >= 8 ? 8 : left > 0 ? static_cast<int>(left) : 0;
-    const bool vec = ((reinterpret_cast<uintptr_t>(e.param) | reinterpret_cast<uintptr_t>(e.grad)) & 15) == 0;
-    PT* const param = static_cast<PT*>(e.param);
-    float g[8], p[8], m[8], v[8];
-    uint2 mc, vc;
-    float ms = 0.f, vs = 0.f;
-    if (EIGHT) {
-      mc = adam_codes(e.m, i);
-      vc = adam_codes(e.v, i);
-      ms = e.m_scale[blk];
-      vs = e.v_scale[blk];
-    } else {
-      adam_get(static_cast<const float*>(e.m), i, cnt, true, m);
-      adam_get(static_cast<const float*>(e.v), i, cnt, true, v);
-    }
-    adam_get(static_cast<const GT*>(e.grad), i, cnt, vec, g);
-    if (MASTER)
-      adam_get(e.master, i, cnt, true, p);
+    d.tensor = lo;
+    d.blk = b - tab.start[lo];
+    int64_t i;
+    int cnt;
+    bool vec;
+    place(e, d.blk, i, cnt, vec);
+    adam_get(d.g, static_cast<const GT*>(e.grad) + i, cnt, vec);
+    if constexpr (MASTER)
+      adam_get(d.p, e.master + i, cnt, true);
     else
-      adam_get(param, i, cnt, vec, p);
+      adam_get(d.p, static_cast<const PT*>(e.param) + i, cnt, vec);
     if (EIGHT) {
-      adam_decode(mc, ms, m);
-      adam_decode(vc, vs, v);
+      d.mc = adam_codes(e.m, i);
+      d.vc = adam_codes(e.v, i);
+      d.ms = e.m_scale[d.blk];
+      d.vs = e.v_scale[d.blk];
+    } else {
+      adam_get(d.m, static_cast<const float*>(e.m) + i, cnt, true);
+      adam_get(d.v, static_cast<const float*>(e.v) + i, cnt, true);
     }
-    float r[8];
+  };
+  auto work = [&](const Loaded& d) {
+    const AdamTensor& e = tab.t[d.tensor];
+    int64_t i;
+    int cnt;
+    bool vec;
+    place(e, d.blk, i, cnt, vec);
+    float g[8], p[8], m[8], v[8], r[8];
+    d.g.get(g);
+    d.p.get(p);
+    if (EIGHT) {
+      adam_decode(d.mc, d.ms, m);
+      adam_decode(d.vc, d.vs, v);
+    } else {
+      d.m.get(m);
+      d.v.get(v);
+    }
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const float gk = __fmul_rn(g[k], gscale);
@@ -286,14 +348,26 @@ __global__ void __launch_bounds__(kAdamThreads)
         for (int k = 0; k < 8; ++k)
           if (k >= cnt) m[k] = r[k] = 0.f;  // past the tensor's end (codes there are padding)
       }
-      adam_encode<false>(m, e.m, i, e.m_scale + blk, lane);
-      adam_encode<true>(r, e.v, i, e.v_scale + blk, lane);
+      adam_encode<false>(m, e.m, i, e.m_scale + d.blk, lane);
+      adam_encode<true>(r, e.v, i, e.v_scale + d.blk, lane);
     } else {
-      adam_put(static_cast<float*>(e.m), i, cnt, true, m);
-      adam_put(static_cast<float*>(e.v), i, cnt, true, v);
+      adam_put(static_cast<float*>(e.m) + i, cnt, true, m);
+      adam_put(static_cast<float*>(e.v) + i, cnt, true, v);
     }
-    if (MASTER) adam_put(e.master, i, cnt, true, p);
-    adam_put(param, i, cnt, vec, p);
+    if (MASTER) adam_put(e.master + i, cnt, true, p);
+    adam_put(static_cast<PT*>(e.param) + i, cnt, vec, p);
+  };
+  int b = first + (threadIdx.x >> 5);
+  if (b < behind) {
+    Loaded now;
+    load(b, now);
+    for (b += kAdamThreads / 32; b < behind; b += kAdamThreads / 32) {
+      Loaded next;
+      load(b, next);
+      work(now);
+      now = next;
+    }
+    work(now);
   }
 
   // The last CTA of the step's last launch advances the step count: every CTA has read it
