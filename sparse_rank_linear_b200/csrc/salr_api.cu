@@ -751,11 +751,14 @@ int launch_q4_kernel(const Q4Params& p, const CUtensorMap* m, int ctas, int dev,
   // The launch may overlap the kernel ahead.  After the t kernel: records, X and B are
   // complete once that kernel lets this one start, and t is waited for.  Else: only records
   // are read before the kernel ahead has completed.
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(p.parts);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = p.parts > 1 ? 2 : 1;
   SALR_TRY(cudaLaunchKernelEx(&cfg, kern, p, m[0], m[1], m[2]));
   return SALR_OK;
 }
@@ -804,22 +807,26 @@ int launch_q4(const void* X, int M, salr_handle h, const void* A, const void* B,
   p.records = (K + kQ4Cols - 1) / kQ4Cols;
   p.total = static_cast<long long>(blocks) * p.records;
   // Every CTA resident at once, the t kernel's beside them.  Equal ranges of the records; but
-  // where those are short (under kQ4LongRange records), every block is cut alike into as many
-  // parts as leave all CTAs resident: a CTA then has one sum to hand over, not two.
+  // where those are short (under kQ4LongRange records), every block is cut alike into up to 8
+  // parts, a cluster: the sums then meet in shared memory.
   const int sms = device_sms(dev);
   const long long beside = R > 0 ? kQ4TParts * ((Q4TLayout<NT>::kSmemBytes + Q4Layout<NT>::kSmemBytes - 1) /
                                                 Q4Layout<NT>::kSmemBytes) : 0;
   const long long slots = std::max<long long>(1, static_cast<long long>(Q4Layout<NT>::kPerSm) * sms - beside);
   const long long most = std::max<long long>(1, p.total / kQ4MinRecords);
   long long grid = std::min(slots, most);
-  if (p.total / grid < kQ4LongRange && blocks <= grid) grid = grid / blocks * blocks;
+  p.parts = 1;
+  if (p.total / grid < kQ4LongRange && blocks <= grid) {
+    p.parts = static_cast<int>(std::min<long long>(8, grid / blocks));
+    grid = static_cast<long long>(p.parts) * blocks;
+  }
   const int ctas = static_cast<int>(grid);
   CUtensorMap m[3], ma, mx;
   std::memset(m, 0, sizeof(m));
   if (!make_block_map(&m[0], X, K, M, 8 * NT, 2 * Q4Layout<NT>::kRecords)) return SALR_ERR_CUDA;
   // scratch: [t][partial sums], where there are any
   const size_t tb = R > 0 ? kQ4MaxTokens * 256 * sizeof(uint16_t) : 0;
-  const bool shared = p.total % ctas != 0 || (p.total / ctas) % p.records != 0;
+  const bool shared = p.parts > 1 ? false : p.total % ctas != 0 || (p.total / ctas) % p.records != 0;
   const size_t pb = shared ? 2 * static_cast<size_t>(ctas) * M * 128 * sizeof(float) : 0;
   uint8_t* mem = nullptr;
   if (tb + pb) SALR_TRY(dev_alloc_async(reinterpret_cast<void**>(&mem), tb + pb, st, kPoolScratch));

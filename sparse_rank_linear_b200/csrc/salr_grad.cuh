@@ -361,7 +361,7 @@ __global__ void __launch_bounds__(kGradThreads)
 // load per flop), the first CTA issues the MMAs for both, and each keeps its 128 x 256 half
 // of the accumulator in its own TMEM, twice, so that the epilogue of a tile overlaps the
 // next one.  Persistent; the tiles of a last, partial round are split along N.
-constexpr int kDxStages = 6;
+constexpr int kDxStages = 4;
 constexpr int kDxStage = 32768;
 constexpr int kDxMaxParts = 4;
 

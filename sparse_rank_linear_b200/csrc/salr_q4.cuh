@@ -111,6 +111,10 @@ __device__ __forceinline__ void q4_turned(uint32_t tile, int step0, int col8, in
   }
 }
 
+// The token (of 8) of fragment column g.  Neighbouring columns are four rows of X apart, whose
+// 16-byte chunks the 128-byte swizzle puts into different halves of the banks.
+__device__ __forceinline__ int q4_token(int g) { return (g >> 1) | ((g & 1) << 2); }
+
 // 16 bytes that are read once, past L1.
 __device__ __forceinline__ uint4 q4_stream16(const void* p) {
   uint4 v;
@@ -214,6 +218,7 @@ __global__ void __launch_bounds__(Q4TLayout<NT>::kThreads)
     }
   } else {
     const bool live = warp * 16 < R;
+    const int tk = q4_token(g);
     int s = 0, ph = 0;
     for (int c = c0; c < c1; ++c) {
       const bool ok = mbar_wait(&ctrl->full[s], ph);
@@ -225,7 +230,7 @@ __global__ void __launch_bounds__(Q4TLayout<NT>::kThreads)
         for (int h = 0; h < 4; ++h) {
           uint32_t a[2][4];
           q4_turned(smem_u32(tile) + (warp >> 2) * 16384, 32 * h, (warp & 3) * 2, lane, a);
-          const uint8_t* x = tile + 32768 + (h >> 1) * NT * 1024 + g * 128 + (((4 * (h & 1) + tl) ^ g) << 4);
+          const uint8_t* x = tile + 32768 + (h >> 1) * NT * 1024 + tk * 128 + (((4 * (h & 1) + tl) ^ tk) << 4);
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             const uint4 v = *reinterpret_cast<const uint4*>(x + n * 1024);
@@ -244,11 +249,11 @@ __global__ void __launch_bounds__(Q4TLayout<NT>::kThreads)
   if (warp < kQ4TWarps) {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      float* d = sums + (8 * n + 2 * tl) * L::kSumRow + warp * 16 + g;
+      float* d = sums + (8 * n + tl) * L::kSumRow + warp * 16 + g;  // tokens tl and tl + 4
       d[0] = acc[n][0];
-      d[L::kSumRow] = acc[n][1];
+      d[4 * L::kSumRow] = acc[n][1];
       d[8] = acc[n][2];
-      d[L::kSumRow + 8] = acc[n][3];
+      d[4 * L::kSumRow + 8] = acc[n][3];
     }
   }
   __syncthreads();
@@ -306,9 +311,12 @@ struct Q4Layout {
   static constexpr int kStage = kXBytes + (kRecords * kQ4MaxRecord + 1023) / 1024 * 1024;
   static constexpr int kStages = NT <= 2 ? 3 : 4;
   static constexpr int kSmemBytes = kStages * kStage + 1024 + 256;
+  static_assert(kStages * kStage >= NT * 8 * 132 * 4, "the stages hold the sums at the end");
   // CTAs per SM that the shared memory admits (1 KB of it is the system's, per CTA)
   static constexpr int kPerSm = 233472 / (kSmemBytes + 1024) > 4 ? 4 : 233472 / (kSmemBytes + 1024);
 };
+
+constexpr int kQ4SumRow = 132;  // floats: 128 rows and a pad
 
 struct Q4Params {
   Q4View w;
@@ -317,6 +325,7 @@ struct Q4Params {
   uint32_t* count;  // [blocks][8 row tiles] arrivals, zero between calls
   int* status;
   int M, R;
+  int parts;        // > 1: clusters of so many CTAs share a row block, one part of its records each
   int records;      // of a row block
   long long total;  // records in all
 };
@@ -338,8 +347,9 @@ __device__ __forceinline__ void q4_record(const uint8_t* x, const uint8_t* rec, 
   const uint8_t* codes = rec + warp * (RT * 512) + lane * 16;
   const uint8_t* scales = rec + 64 * COLS + (warp * RT * 8 + g) * 4;
   const uint8_t* zeros = rec + 64 * COLS + COLS / GROUP * 256 + (warp * RT * 8 + g) * 2;
-  // token 8n + g, 16-byte chunks tl and 4 + tl of its 64 columns, swizzled
-  const uint8_t* const xh[2] = {x + g * 128 + ((tl ^ g) << 4), x + g * 128 + (((4 + tl) ^ g) << 4)};
+  // this lane's token of each 8, 16-byte chunks tl and 4 + tl of its 64 columns, swizzled
+  const int tk = q4_token(g);
+  const uint8_t* const xh[2] = {x + tk * 128 + ((tl ^ tk) << 4), x + tk * 128 + (((4 + tl) ^ tk) << 4)};
   float cc[RT][NT][4];
 #pragma unroll
   for (int b = 0; b < COLS / 64; ++b) {
@@ -405,12 +415,185 @@ __device__ __forceinline__ void q4_record(const uint8_t* x, const uint8_t* rec, 
   }
 }
 
+// A consumer warp: its row tiles of every segment of the CTA's range.
+template <int NT, int GROUP, bool ZEROS>
+__device__ __forceinline__ void q4_consume(const Q4Params& p, uint8_t* smem, Q4Ctrl* ctrl, long long i0, long long i1,
+                                           int ranks, int warp, int lane) {
+  using L = Q4Layout<NT>;
+  constexpr int RT = L::RT;
+  constexpr int kRecord = 64 * kQ4Cols + kQ4Cols / GROUP * (ZEROS ? 384 : 256);  // bytes
+  const int cta = blockIdx.x, ctas = gridDim.x;
+  const int g = lane >> 2, tl = lane & 3, tk = q4_token(g);
+  const uint32_t mask = q4_opaque(0x000f000fu), one28 = q4_opaque(0x43004300u), eight = q4_opaque(0x43084308u);
+  int s = 0, ph = 0;
+  for (long long i = i0; i < i1;) {
+    const int block = static_cast<int>(i / p.records), c0 = static_cast<int>(i - static_cast<long long>(block) * p.records);
+    const int n = static_cast<int>(min(static_cast<long long>(p.records - c0), i1 - i));
+    const int stages = (n + L::kRecords - 1) / L::kRecords, extra = c0 == 0 ? ranks : 0;
+    float acc[RT][NT][4];
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int k = 0; k < NT; ++k) acc[r][k][0] = acc[r][k][1] = acc[r][k][2] = acc[r][k][3] = 0.f;
+    // records of 128 columns yet to come in this segment; a shorter one ends the block
+    int wide = c0 + n == p.records && p.w.K % kQ4Cols ? n - 1 : n;
+    const bool narrow = wide < n;
+    for (int c = 0; c < stages + extra; ++c) {
+      const bool ok = mbar_wait(&ctrl->full[s], ph);
+      if (!__all_sync(0xffffffffu, ok)) {
+        q4_abort(p.status, ctrl);
+        break;
+      }
+      const uint8_t* x = smem + s * L::kStage;
+      const uint8_t* rec = x + L::kXBytes;
+      if (c < stages) {
+#pragma unroll
+        for (int k = 0; k < L::kRecords; ++k, --wide) {
+          if (wide > 0)
+            q4_record<NT, GROUP, ZEROS, kQ4Cols>(x + k * 2 * L::kXHalf, rec + k * kRecord, warp, lane, mask, one28,
+                                                 eight, acc);
+          else if (GROUP < 128 && narrow && wide == 0)
+            q4_record<NT, GROUP, ZEROS, GROUP == 128 ? 128 : 64>(x + k * 2 * L::kXHalf, rec + k * kRecord, warp,
+                                                                 lane, mask, one28, eight, acc);
+        }
+      } else {
+        uint32_t a[RT][2][4];
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+          const int row = (warp * RT + r) * 16;
+          q4_turned(smem_u32(rec) + (row >> 6) * 4096, 0, (row & 63) >> 3, lane, a[r]);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)  // t's two parts
+#pragma unroll
+          for (int k = 0; k < NT; ++k) {
+            const uint4 v = *reinterpret_cast<const uint4*>(x + k * 1024 + tk * 128 + (((4 * h + tl) ^ tk) << 4));
+#pragma unroll
+            for (int r = 0; r < RT; ++r) {
+              mma_m16n8k16(acc[r][k], a[r][0], v.x, v.y);
+              mma_m16n8k16(acc[r][k], a[r][1], v.z, v.w);
+            }
+          }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctrl->empty[s]);
+      if (++s == L::kStages) s = 0, ph ^= 1;
+    }
+    if (p.parts > 1) {  // the CTAs of the cluster add them up together
+      named_bar(1, 32 * L::kWarps);  // every consumer is through with the ring
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int k = 0; k < NT; ++k) {
+          float* d = reinterpret_cast<float*>(smem) + (8 * k + tl) * kQ4SumRow + (warp * RT + r) * 16 + g;
+          d[0] = acc[r][k][0];
+          d[4 * kQ4SumRow] = acc[r][k][1];
+          d[8] = acc[r][k][2];
+          d[4 * kQ4SumRow + 8] = acc[r][k][3];
+        }
+      return;
+    }
+    if (q4_aborted(ctrl)) return;  // the values are not whole: nothing of the block is written
+    // this warp's rows of the block: values (row, token) at 4 places of each 16 x 8 tile
+    const size_t n0 = static_cast<size_t>(block) * 128;
+    int place = 0;
+    auto each = [&](auto&& f, int& j) {
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int k = 0; k < NT; ++k)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int m = 8 * k + tl + 4 * (e & 1), row = (warp * RT + r) * 16 + g + 8 * (e >> 1);
+            j = (r * NT + k) * 4 + e;
+            if (m < p.M) f(acc[r][k][e], m, row);
+          }
+    };
+    auto store = [&](float v, int m, int row) {
+      reinterpret_cast<__nv_bfloat16*>(p.Y)[static_cast<size_t>(m) * p.w.N + n0 + row] = __float2bfloat16_rn(v);
+    };
+    if (n == p.records) {
+      each(store, place);
+    } else {
+      const size_t slot = static_cast<size_t>(p.M) * 128;
+      // a block that the range starts in takes the CTA's slot 0, one that it ends in slot 1
+      float* mine = p.part + (2 * static_cast<size_t>(cta) + (i == i0 ? 0 : 1)) * slot;
+      each([&](float v, int m, int row) { __stcg(mine + m * 128 + row, v); }, place);
+      __threadfence();
+      __syncwarp();
+      const long long b0 = static_cast<long long>(block) * p.records;
+      const int f = q4_owner(p.total, b0, ctas), l = q4_owner(p.total, b0 + p.records - 1, ctas);
+      uint32_t last = 0;
+      if (lane == 0) last = atomicAdd(p.count + block * 8 + warp, 1u) == static_cast<uint32_t>(l - f);
+      if (__shfl_sync(0xffffffffu, last, 0)) {
+        __threadfence();
+        // the first CTA of the block has it in slot 1 unless its range starts with the block
+        const float* from = p.part + (2 * static_cast<size_t>(f) + (q4_range(p.total, f, ctas) == b0 ? 0 : 1)) * slot;
+        each([&](float& v, int m, int row) { v = __ldcg(from + m * 128 + row); }, place);
+        const float* next = p.part + 2 * static_cast<size_t>(f + 1) * slot;
+        int c = f + 1;
+        // the values of several ranges at once: one trip to L2 for all of them
+        constexpr int kAtOnce = NT <= 2 ? 4 : 1;
+        for (; c + kAtOnce <= l + 1; c += kAtOnce, next += 2 * kAtOnce * slot) {
+          float v[kAtOnce][RT * NT * 4];
+#pragma unroll
+          for (int k = 0; k < kAtOnce; ++k) {
+            int j = 0;
+            each([&](float&, int m, int row) { v[k][j] = __ldcg(next + 2 * k * slot + m * 128 + row); }, j);
+          }
+#pragma unroll
+          for (int k = 0; k < kAtOnce; ++k) {
+            int j = 0;
+            each([&](float& a, int, int) { a += v[k][j]; }, j);
+          }
+        }
+        for (; c <= l; ++c, next += 2 * slot)
+          each([&](float& v, int m, int row) { v += __ldcg(next + m * 128 + row); }, place);
+        each(store, place);
+        if (lane == 0) p.count[block * 8 + warp] = 0u;
+      }
+    }
+    i += n;
+  }
+}
+
+// The sums of a cluster's CTAs, which lie in their shared memory ([token][132]): each CTA adds
+// up and writes its share of the row block's values, in the order of the parts.
+template <int NT>
+__device__ __forceinline__ void q4_join(const Q4Params& p, uint8_t* smem, Q4Ctrl* ctrl, int block) {
+  const int part = blockIdx.x % p.parts;
+  __syncthreads();
+  cluster_sync_all();
+  if (!q4_aborted(ctrl)) {
+    const int all = p.M * 64;  // pairs of rows
+    const uint32_t base = smem_u32(smem);
+    for (int i = part * all / p.parts + threadIdx.x; i < (part + 1) * all / p.parts; i += Q4Layout<NT>::kThreads) {
+      const int m = i >> 6, row = 2 * (i & 63);
+      const uint32_t at = base + (m * kQ4SumRow + row) * 4;
+      float x[8][2], v0 = 0.f, v1 = 0.f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        x[k][0] = x[k][1] = 0.f;
+        if (k < p.parts)
+          asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
+                       : "=f"(x[k][0]), "=f"(x[k][1])
+                       : "r"(map_to_rank(at, k)));
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v0 += x[k][0], v1 += x[k][1];
+      *reinterpret_cast<__nv_bfloat162*>(p.Y + static_cast<size_t>(m) * p.w.N + block * 128 + row) =
+          __floats2bfloat162_rn(v0, v1);
+    }
+  }
+  __syncthreads();
+  cluster_sync_all();  // no CTA leaves while another may still read its sums
+}
+
 template <int NT, int GROUP, bool ZEROS>
 __global__ void __launch_bounds__(Q4Layout<NT>::kThreads, Q4Layout<NT>::kPerSm)
     q4_linear_kernel(const __grid_constant__ Q4Params p, const __grid_constant__ CUtensorMap mx,
                      const __grid_constant__ CUtensorMap mt, const __grid_constant__ CUtensorMap mb) {
   using L = Q4Layout<NT>;
-  constexpr int RT = L::RT;
   constexpr int kRecord = 64 * kQ4Cols + kQ4Cols / GROUP * (ZEROS ? 384 : 256);  // bytes
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align_1024(smem_raw);
@@ -489,127 +672,10 @@ __global__ void __launch_bounds__(Q4Layout<NT>::kThreads, Q4Layout<NT>::kPerSm)
           mbar_wait(&ctrl->full[k % L::kStages], (k / L::kStages) & 1);
       if (p.R > 0 && !waited) griddep_wait();  // this grid ends after the t kernel
     }
-    return;
+  } else {
+    q4_consume<NT, GROUP, ZEROS>(p, smem, ctrl, i0, i1, ranks, warp, lane);
   }
-
-  const int g = lane >> 2, tl = lane & 3;
-  const uint32_t mask = q4_opaque(0x000f000fu), one28 = q4_opaque(0x43004300u), eight = q4_opaque(0x43084308u);
-  int s = 0, ph = 0;
-  for (long long i = i0; i < i1;) {
-    const int block = static_cast<int>(i / p.records), c0 = static_cast<int>(i - static_cast<long long>(block) * p.records);
-    const int n = static_cast<int>(min(static_cast<long long>(p.records - c0), i1 - i));
-    const int stages = (n + L::kRecords - 1) / L::kRecords, extra = c0 == 0 ? ranks : 0;
-    float acc[RT][NT][4];
-#pragma unroll
-    for (int r = 0; r < RT; ++r)
-#pragma unroll
-      for (int k = 0; k < NT; ++k) acc[r][k][0] = acc[r][k][1] = acc[r][k][2] = acc[r][k][3] = 0.f;
-    // records of 128 columns yet to come in this segment; a shorter one ends the block
-    int wide = c0 + n == p.records && p.w.K % kQ4Cols ? n - 1 : n;
-    const bool narrow = wide < n;
-    for (int c = 0; c < stages + extra; ++c) {
-      const bool ok = mbar_wait(&ctrl->full[s], ph);
-      if (!__all_sync(0xffffffffu, ok)) {
-        q4_abort(p.status, ctrl);
-        return;
-      }
-      const uint8_t* x = smem + s * L::kStage;
-      const uint8_t* rec = x + L::kXBytes;
-      if (c < stages) {
-#pragma unroll
-        for (int k = 0; k < L::kRecords; ++k, --wide) {
-          if (wide > 0)
-            q4_record<NT, GROUP, ZEROS, kQ4Cols>(x + k * 2 * L::kXHalf, rec + k * kRecord, warp, lane, mask, one28,
-                                                 eight, acc);
-          else if (GROUP < 128 && narrow && wide == 0)
-            q4_record<NT, GROUP, ZEROS, GROUP == 128 ? 128 : 64>(x + k * 2 * L::kXHalf, rec + k * kRecord, warp,
-                                                                 lane, mask, one28, eight, acc);
-        }
-      } else {
-        uint32_t a[RT][2][4];
-#pragma unroll
-        for (int r = 0; r < RT; ++r) {
-          const int row = (warp * RT + r) * 16;
-          q4_turned(smem_u32(rec) + (row >> 6) * 4096, 0, (row & 63) >> 3, lane, a[r]);
-        }
-#pragma unroll
-        for (int h = 0; h < 2; ++h)  // t's two parts
-#pragma unroll
-          for (int k = 0; k < NT; ++k) {
-            const uint4 v = *reinterpret_cast<const uint4*>(x + k * 1024 + g * 128 + (((4 * h + tl) ^ g) << 4));
-#pragma unroll
-            for (int r = 0; r < RT; ++r) {
-              mma_m16n8k16(acc[r][k], a[r][0], v.x, v.y);
-              mma_m16n8k16(acc[r][k], a[r][1], v.z, v.w);
-            }
-          }
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ctrl->empty[s]);
-      if (++s == L::kStages) s = 0, ph ^= 1;
-    }
-    if (q4_aborted(ctrl)) return;  // the values are not whole: nothing of the block is written
-    // this warp's rows of the block: values (row, token) at 4 places of each 16 x 8 tile
-    const size_t n0 = static_cast<size_t>(block) * 128;
-    int place = 0;
-    auto each = [&](auto&& f, int& j) {
-#pragma unroll
-      for (int r = 0; r < RT; ++r)
-#pragma unroll
-        for (int k = 0; k < NT; ++k)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int m = 8 * k + 2 * tl + (e & 1), row = (warp * RT + r) * 16 + g + 8 * (e >> 1);
-            j = (r * NT + k) * 4 + e;
-            if (m < p.M) f(acc[r][k][e], m, row);
-          }
-    };
-    auto store = [&](float v, int m, int row) {
-      reinterpret_cast<__nv_bfloat16*>(p.Y)[static_cast<size_t>(m) * p.w.N + n0 + row] = __float2bfloat16_rn(v);
-    };
-    if (n == p.records) {
-      each(store, place);
-    } else {
-      const size_t slot = static_cast<size_t>(p.M) * 128;
-      // a block that the range starts in takes the CTA's slot 0, one that it ends in slot 1
-      float* mine = p.part + (2 * static_cast<size_t>(cta) + (i == i0 ? 0 : 1)) * slot;
-      each([&](float v, int m, int row) { __stcg(mine + m * 128 + row, v); }, place);
-      __threadfence();
-      __syncwarp();
-      const long long b0 = static_cast<long long>(block) * p.records;
-      const int f = q4_owner(p.total, b0, ctas), l = q4_owner(p.total, b0 + p.records - 1, ctas);
-      uint32_t last = 0;
-      if (lane == 0) last = atomicAdd(p.count + block * 8 + warp, 1u) == static_cast<uint32_t>(l - f);
-      if (__shfl_sync(0xffffffffu, last, 0)) {
-        __threadfence();
-        // the first CTA of the block has it in slot 1 unless its range starts with the block
-        const float* from = p.part + (2 * static_cast<size_t>(f) + (q4_range(p.total, f, ctas) == b0 ? 0 : 1)) * slot;
-        each([&](float& v, int m, int row) { v = __ldcg(from + m * 128 + row); }, place);
-        const float* next = p.part + 2 * static_cast<size_t>(f + 1) * slot;
-        int c = f + 1;
-        // the values of several ranges at once: one trip to L2 for all of them
-        constexpr int kAtOnce = NT <= 2 ? 4 : 1;
-        for (; c + kAtOnce <= l + 1; c += kAtOnce, next += 2 * kAtOnce * slot) {
-          float v[kAtOnce][RT * NT * 4];
-#pragma unroll
-          for (int k = 0; k < kAtOnce; ++k) {
-            int j = 0;
-            each([&](float&, int m, int row) { v[k][j] = __ldcg(next + 2 * k * slot + m * 128 + row); }, j);
-          }
-#pragma unroll
-          for (int k = 0; k < kAtOnce; ++k) {
-            int j = 0;
-            each([&](float& a, int, int) { a += v[k][j]; }, j);
-          }
-        }
-        for (; c <= l; ++c, next += 2 * slot)
-          each([&](float& v, int m, int row) { v += __ldcg(next + m * 128 + row); }, place);
-        each(store, place);
-        if (lane == 0) p.count[block * 8 + warp] = 0u;
-      }
-    }
-    i += n;
-  }
+  if (p.parts > 1) q4_join<NT>(p, smem, ctrl, static_cast<int>(i0 / p.records));
 }
 
 // ------------------------------------------------------------------------------------
