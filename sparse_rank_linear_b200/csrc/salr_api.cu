@@ -729,20 +729,81 @@ int check_linear_args(const void* X, int64_t M, salr_handle h, const void* A, co
   return SALR_OK;
 }
 
+// CTAs of the layer kernel whose room a CTA of the t kernel takes.
+template <int NT>
+constexpr int q4_beside() {
+  return (Q4TLayout<NT>::kSmemBytes + Q4Layout<NT>::kSmemBytes - 1) / Q4Layout<NT>::kSmemBytes;
+}
+
 // Fewest records of a CTA's range (below, its set-up and the sums' meeting cost more than
 // the records).
 constexpr int kQ4MinRecords = 4;
 constexpr int kQ4LongRange = 16;
 
-template <int NT, int GROUP, bool ZEROS>
-int launch_q4_kernel(const Q4Params& p, const CUtensorMap* m, int ctas, int dev, cudaStream_t st) {
+// Clusters of each size that a kernel has resident at once on a device (1 .. 8 CTAs): they
+// stay within a GPC, so fewer fit than CTAs do.
+struct ClusterRoom {
+  std::atomic<int> known[64];  // zero-initialised: not looked up yet
+  int room[64][9];
+};
+
+template <typename Kernel>
+int cluster_room(ClusterRoom& c, Kernel kern, int threads, int smem, int dev, int size) {
+  static std::mutex mu;
+  if (!c.known[dev]) {
+    std::lock_guard<std::mutex> g(mu);
+    for (int k = 1; k <= 8 && !c.known[dev]; ++k) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(static_cast<unsigned>(k));
+      cfg.blockDim = dim3(static_cast<unsigned>(threads));
+      cfg.dynamicSmemBytes = smem;
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = static_cast<unsigned>(k);
+      attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      int n = 0;
+      if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) n = 0;
+      c.room[dev][k] = n;
+    }
+    c.known[dev] = 1;
+  }
+  return c.room[dev][size];
+}
+
+// `t_first` launches the t kernel (or does nothing): nothing may be queued between it and the
+// layer kernel.
+template <int NT, int GROUP, bool ZEROS, typename F>
+int launch_q4_kernel(Q4Params p, const CUtensorMap* m, F&& t_first, cudaStream_t st) {
   using L = Q4Layout<NT>;
   const auto kern = q4_linear_kernel<NT, GROUP, ZEROS>;
   static std::atomic<bool> attr_set[64];  // zero-initialised: false
+  static ClusterRoom room;
+  int dev = 0;
+  SALR_TRY(cudaGetDevice(&dev));
+  if (dev < 0 || dev >= 64) return SALR_ERR_UNSUPPORTED;
   if (!attr_set[dev]) {
     SALR_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmemBytes));
     attr_set[dev] = true;
   }
+  // Every CTA resident at once, the t kernel's beside them.  Equal ranges of the records; but
+  // where those are short (under kQ4LongRange records), every block is cut alike into up to 8
+  // parts, a cluster: the sums then meet in shared memory.
+  const int blocks = p.w.N / 128, beside = p.R > 0 ? kQ4TParts * q4_beside<NT>() : 0;
+  const long long slots = std::max(1, L::kPerSm * device_sms(dev) - beside);
+  const long long grid = std::max<long long>(1, std::min(slots, p.total / kQ4MinRecords));
+  p.parts = 1;
+  if (p.total / grid < kQ4LongRange)
+    for (int k = 2; k <= 8 && k * kQ4MinRecords <= p.records; ++k)
+      if (blocks <= cluster_room(room, kern, L::kThreads, L::kSmemBytes, dev, k) - (beside + k - 1) / k) p.parts = k;
+  const int ctas = p.parts > 1 ? p.parts * blocks : static_cast<int>(grid);
+  // sums that meet in L2: [CTAs x 2][M][128]
+  const bool meet = p.parts == 1 && (p.total % ctas != 0 || (p.total / ctas) % p.records != 0);
+  void* sums = nullptr;
+  if (meet)
+    SALR_TRY(dev_alloc_async(&sums, 2 * static_cast<size_t>(ctas) * p.M * 128 * sizeof(float), st, kPoolScratch));
+  p.part = static_cast<float*>(sums);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(ctas));
   cfg.blockDim = dim3(L::kThreads);
@@ -759,8 +820,10 @@ int launch_q4_kernel(const Q4Params& p, const CUtensorMap* m, int ctas, int dev,
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = p.parts > 1 ? 2 : 1;
-  SALR_TRY(cudaLaunchKernelEx(&cfg, kern, p, m[0], m[1], m[2]));
-  return SALR_OK;
+  int rc = t_first();
+  if (rc == SALR_OK) rc = cuda_status(cudaLaunchKernelEx(&cfg, kern, p, m[0], m[1], m[2]));
+  const cudaError_t f = sums ? cudaFreeAsync(sums, st) : cudaSuccess;
+  return rc != SALR_OK ? rc : cuda_status(f);
 }
 
 template <int NT>
@@ -806,49 +869,27 @@ int launch_q4(const void* X, int M, salr_handle h, const void* A, const void* B,
   p.R = R;
   p.records = (K + kQ4Cols - 1) / kQ4Cols;
   p.total = static_cast<long long>(blocks) * p.records;
-  // Every CTA resident at once, the t kernel's beside them.  Equal ranges of the records; but
-  // where those are short (under kQ4LongRange records), every block is cut alike into up to 8
-  // parts, a cluster: the sums then meet in shared memory.
-  const int sms = device_sms(dev);
-  const long long beside = R > 0 ? kQ4TParts * ((Q4TLayout<NT>::kSmemBytes + Q4Layout<NT>::kSmemBytes - 1) /
-                                                Q4Layout<NT>::kSmemBytes) : 0;
-  const long long slots = std::max<long long>(1, static_cast<long long>(Q4Layout<NT>::kPerSm) * sms - beside);
-  const long long most = std::max<long long>(1, p.total / kQ4MinRecords);
-  long long grid = std::min(slots, most);
-  p.parts = 1;
-  if (p.total / grid < kQ4LongRange && blocks <= grid) {
-    p.parts = static_cast<int>(std::min<long long>(8, grid / blocks));
-    grid = static_cast<long long>(p.parts) * blocks;
-  }
-  const int ctas = static_cast<int>(grid);
   CUtensorMap m[3], ma, mx;
   std::memset(m, 0, sizeof(m));
   if (!make_block_map(&m[0], X, K, M, 8 * NT, 2 * Q4Layout<NT>::kRecords)) return SALR_ERR_CUDA;
-  // scratch: [t][partial sums], where there are any
-  const size_t tb = R > 0 ? kQ4MaxTokens * 256 * sizeof(uint16_t) : 0;
-  const bool shared = p.parts > 1 ? false : p.total % ctas != 0 || (p.total / ctas) % p.records != 0;
-  const size_t pb = shared ? 2 * static_cast<size_t>(ctas) * M * 128 * sizeof(float) : 0;
-  uint8_t* mem = nullptr;
-  if (tb + pb) SALR_TRY(dev_alloc_async(reinterpret_cast<void**>(&mem), tb + pb, st, kPoolScratch));
-  p.part = reinterpret_cast<float*>(mem + tb);
+  uint8_t* mem = nullptr;  // t
+  if (R > 0)
+    SALR_TRY(dev_alloc_async(reinterpret_cast<void**>(&mem), kQ4MaxTokens * 256 * sizeof(uint16_t), st, kPoolScratch));
+  uint16_t* t = reinterpret_cast<uint16_t*>(mem);
+  auto t_first = [&]() -> int { return R > 0 ? launch_q4_t<NT>(mx, ma, M, K, R, t, h->status, dev, st) : SALR_OK; };
   auto run = [&]() -> int {
-    if (R > 0) {
-      // t rows past M are not written: their products belong to no token
-      uint16_t* t = reinterpret_cast<uint16_t*>(mem);
-      if (!make_map(&m[1], t, 256, M, 64, 8 * NT) || !make_map(&m[2], B, h->N, R, 64, 32) ||
-          !make_block_map(&mx, X, K, M, 8 * NT, 2) || !make_map(&ma, A, R, K, 64, 128))
-        return SALR_ERR_CUDA;
-      const int rc = launch_q4_t<NT>(mx, ma, M, K, R, t, h->status, dev, st);
-      if (rc != SALR_OK) return rc;
-    }
+    // t rows past M are not written, and read as zero
+    if (R > 0 && (!make_map(&m[1], t, 256, M, 64, 8 * NT) || !make_map(&m[2], B, h->N, R, 64, 32) ||
+                  !make_block_map(&mx, X, K, M, 8 * NT, 2) || !make_map(&ma, A, R, K, 64, 128)))
+      return SALR_ERR_CUDA;
     const int g = h->group;
     if (p.w.zeros)
-      return g == 32   ? launch_q4_kernel<NT, 32, true>(p, m, ctas, dev, st)
-             : g == 64 ? launch_q4_kernel<NT, 64, true>(p, m, ctas, dev, st)
-                       : launch_q4_kernel<NT, 128, true>(p, m, ctas, dev, st);
-    return g == 32   ? launch_q4_kernel<NT, 32, false>(p, m, ctas, dev, st)
-           : g == 64 ? launch_q4_kernel<NT, 64, false>(p, m, ctas, dev, st)
-                     : launch_q4_kernel<NT, 128, false>(p, m, ctas, dev, st);
+      return g == 32   ? launch_q4_kernel<NT, 32, true>(p, m, t_first, st)
+             : g == 64 ? launch_q4_kernel<NT, 64, true>(p, m, t_first, st)
+                       : launch_q4_kernel<NT, 128, true>(p, m, t_first, st);
+    return g == 32   ? launch_q4_kernel<NT, 32, false>(p, m, t_first, st)
+           : g == 64 ? launch_q4_kernel<NT, 64, false>(p, m, t_first, st)
+                     : launch_q4_kernel<NT, 128, false>(p, m, t_first, st);
   };
   const int rc = run();
   const cudaError_t e = mem ? cudaFreeAsync(mem, st) : cudaSuccess;

@@ -655,11 +655,11 @@ __global__ void __launch_bounds__(Q4Layout<NT>::kThreads, Q4Layout<NT>::kPerSm)
             }
           } else {
             const int a = c - stages;
-            if (!waited) griddep_wait();  // t
-            waited = true;
             mbar_arrive_expect_tx(bar, 8192 + L::kXHalf);
             tma_load_2d(dst, &mb, block * 128, a * 32, bar);
             tma_load_2d(dst + 4096, &mb, block * 128 + 64, a * 32, bar);
+            if (!waited) griddep_wait();  // t
+            waited = true;
             tma_load_2d(x, &mt, a * 64, 0, bar);
           }
           ++issued;
