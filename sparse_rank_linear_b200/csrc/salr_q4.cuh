@@ -19,8 +19,8 @@
 // both operands agree, and a product stays within 32 columns (groups of 32).
 //
 // Arithmetic: 0x4300 | q is bf16 128 + q; minus the bf16 128 + z it is q - z, exactly.  The
-// products q x are exact in fp32 and accumulate in fp32 over a group, which is then scaled
-// in fp32.  t = X A is summed in fp32 and enters the adapter's product with 16 bits of
+// products q x are exact in fp32 and accumulate in fp32 over a group (64 columns of it, if it
+// is longer), which is then scaled in fp32.  t = X A is summed in fp32 and enters the adapter's product with 16 bits of
 // significand.  Y is rounded once.
 //
 // Bound: HBM, by the codes (0.5 byte per weight plus scales), up to about 20 tokens; above,
@@ -306,10 +306,10 @@ struct Q4Layout {
   static constexpr int kXHalf = NT * 1024;  // 8 NT tokens x 64 columns
   // Records to a stage: with few tokens a record is so little work that the stage's
   // handshake would take a third of the instructions.
-  static constexpr int kRecords = NT <= 2 ? 2 : 1;
+  static constexpr int kRecords = NT <= 4 ? 2 : 1;
   static constexpr int kXBytes = 2 * kRecords * kXHalf;
   static constexpr int kStage = kXBytes + (kRecords * kQ4MaxRecord + 1023) / 1024 * 1024;
-  static constexpr int kStages = NT <= 2 ? 3 : 4;
+  static constexpr int kStages = NT <= 4 ? 3 : 4;
   static constexpr int kSmemBytes = kStages * kStage + 1024 + 256;
   static_assert(kStages * kStage >= NT * 8 * 132 * 4, "the stages hold the sums at the end");
   // CTAs per SM that the shared memory admits (1 KB of it is the system's, per CTA)
@@ -350,65 +350,71 @@ __device__ __forceinline__ void q4_record(const uint8_t* x, const uint8_t* rec, 
   // this lane's token of each 8, 16-byte chunks tl and 4 + tl of its 64 columns, swizzled
   const int tk = q4_token(g);
   const uint8_t* const xh[2] = {x + tk * 128 + ((tl ^ tk) << 4), x + tk * 128 + (((4 + tl) ^ tk) << 4)};
-  float cc[RT][NT][4];
+  // tokens taken at once (of 8 each): their products do not wait for one another, and the
+  // fragments of all NT would not fit the registers
+  constexpr int NC = NT < 2 ? NT : 2;
 #pragma unroll
   for (int b = 0; b < COLS / 64; ++b) {
-    uint4 code[RT];
+    uint32_t a[RT][2][2][4];  // [row tile][32 columns][product]
+    float sl[RT][2], sh[RT][2];
 #pragma unroll
-    for (int r = 0; r < RT; ++r) code[r] = *reinterpret_cast<const uint4*>(codes + b * 4096 + r * 512);
+    for (int r = 0; r < RT; ++r) {
+      const uint4 code = *reinterpret_cast<const uint4*>(codes + b * 4096 + r * 512);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {  // 32 columns, two products
-      const int grp = (b * 64 + h * 32) / GROUP;
-      const bool first = (b * 64 + h * 32) % GROUP == 0;
-      const bool end = (b * 64 + h * 32 + 32) % GROUP == 0;
-      uint32_t a[RT][2][4];
-#pragma unroll
-      for (int r = 0; r < RT; ++r) {
+      for (int h = 0; h < 2; ++h) {
+        const int grp = (b * 64 + h * 32) / GROUP;
         uint32_t lo = eight, hi = eight;
         if (ZEROS) {
           const uint32_t z = *reinterpret_cast<const uint16_t*>(zeros + grp * 128 + r * 16);
           lo = q4_bias(z, 0);
           hi = q4_bias(z, 1);
         }
-        const uint32_t w0 = h ? code[r].y : code[r].x, w1 = h ? code[r].w : code[r].z;
+        const uint32_t w0 = h ? code.y : code.x, w1 = h ? code.w : code.z;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const int sh = 4 * (2 * i + j);
-            a[r][i][2 * j] = q4_sub2(q4_pair(w0 >> sh, mask, one28), lo);
-            a[r][i][2 * j + 1] = q4_sub2(q4_pair(w1 >> sh, mask, one28), hi);
+            const int at = 4 * (2 * i + j);
+            a[r][h][i][2 * j] = q4_sub2(q4_pair(w0 >> at, mask, one28), lo);
+            a[r][h][i][2 * j + 1] = q4_sub2(q4_pair(w1 >> at, mask, one28), hi);
           }
+        const uint32_t s2 = *reinterpret_cast<const uint32_t*>(scales + grp * 256 + r * 32);
+        sl[r][h] = __uint_as_float(s2 << 16);
+        sh[r][h] = __uint_as_float(s2 & 0xffff0000u);
       }
-      uint4 v[NT];
+    }
 #pragma unroll
-      for (int n = 0; n < NT; ++n) v[n] = *reinterpret_cast<const uint4*>(xh[h] + b * L::kXHalf + n * 1024);
-      // all first products, then all second ones: neighbours do not wait for one another
+    for (int n0 = 0; n0 < NT; n0 += NC) {
+      float cc[RT][NC][4];
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+      for (int h = 0; h < 2; ++h) {
+        uint4 v[NC];
 #pragma unroll
-        for (int r = 0; r < RT; ++r) {
-          if (first)
-            mma_m16n8k16_zero(cc[r][n], a[r][0], v[n].x, v[n].y);
-          else
-            mma_m16n8k16(cc[r][n], a[r][0], v[n].x, v[n].y);
-        }
+        for (int n = 0; n < NC; ++n) v[n] = *reinterpret_cast<const uint4*>(xh[h] + b * L::kXHalf + (n0 + n) * 1024);
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+        for (int r = 0; r < RT; ++r)
 #pragma unroll
-        for (int r = 0; r < RT; ++r) mma_m16n8k16(cc[r][n], a[r][1], v[n].z, v[n].w);
-      if (end) {
-#pragma unroll
-        for (int r = 0; r < RT; ++r) {
-          const uint32_t s2 = *reinterpret_cast<const uint32_t*>(scales + grp * 256 + r * 32);
-          const float sl = __uint_as_float(s2 << 16), sh = __uint_as_float(s2 & 0xffff0000u);
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            acc[r][n][0] = fmaf(sl, cc[r][n][0], acc[r][n][0]);
-            acc[r][n][1] = fmaf(sl, cc[r][n][1], acc[r][n][1]);
-            acc[r][n][2] = fmaf(sh, cc[r][n][2], acc[r][n][2]);
-            acc[r][n][3] = fmaf(sh, cc[r][n][3], acc[r][n][3]);
+          for (int n = 0; n < NC; ++n) {
+            if (h == 0 || GROUP == 32)
+              mma_m16n8k16_zero(cc[r][n], a[r][h][0], v[n].x, v[n].y);
+            else
+              mma_m16n8k16(cc[r][n], a[r][h][0], v[n].x, v[n].y);
           }
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+          for (int n = 0; n < NC; ++n) mma_m16n8k16(cc[r][n], a[r][h][1], v[n].z, v[n].w);
+        if (h == 1 || GROUP == 32) {
+#pragma unroll
+          for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int n = 0; n < NC; ++n) {
+              float(&d)[4] = acc[r][n0 + n];
+              d[0] = fmaf(sl[r][h], cc[r][n][0], d[0]);
+              d[1] = fmaf(sl[r][h], cc[r][n][1], d[1]);
+              d[2] = fmaf(sh[r][h], cc[r][n][2], d[2]);
+              d[3] = fmaf(sh[r][h], cc[r][n][3], d[3]);
+            }
         }
       }
     }

@@ -73,19 +73,22 @@ def bf16(g, *shape, scale=1.0):
 
 
 def check_small(Y, X, W, A, B, group):
-    """|Y - Y*| <= half a bf16 step + the fp32 sums' error.  With S the sum of |products|: a
-    group adds group / 16 products of 16 values, at most 17 roundings each (2^-23: the tensor
-    cores may truncate); a warp then adds an eighth of the groups' sums and of the R adapter
-    products, and 8 partial sums meet; the scale, t (K terms over 256 threads and a tree) and
-    the rest stay within 16 + K / 256 more."""
+    """|Y - Y*| <= half a bf16 step + the fp32 sums' error.  With S the sum of |products|: 64
+    columns (32, if the group is that) are at most 4 products of 16, 17 roundings each (2^-23:
+    the tensor cores may truncate); their scaled sums are added one after another (2^-24
+    each), K / 64 or K / 32 of them; the adapter adds 2 R / 16 products on top, its t (K / 16
+    products) is kept to 2^-16, and the partial sums of a row's ranges are fewer than 64."""
     K, R = X.shape[1], 0 if A is None else A.shape[1]
     Xd = X.double()
     Y64, S = Xd @ W.t(), Xd.abs() @ W.abs().t()
     if R:
         Y64 = Y64 + (Xd @ A.double()) @ B.double()
         S = S + (Xd.abs() @ A.double().abs()) @ B.double().abs()
-    n = 17 * group / 16 + K / (8 * group) + R / 8 + 16 + K / 256
+    n = 4 * 17 + K / min(group, 64) / 2 + 64
     tol = 2.0 ** -8 * Y64.abs() + n * 2.0 ** -23 * S
+    if R:
+        Sa = (Xd.abs() @ A.double().abs()) @ B.double().abs()
+        tol = tol + (2.0 ** -16 + 2.0 ** -23 * (17 * (K / 16 + R / 8))) * Sa
     err = (Y.double() - Y64).abs()
     assert (err <= tol).all(), f"worst {(err / tol).max().item():.3f} of the tolerance"
 
