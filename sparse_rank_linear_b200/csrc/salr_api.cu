@@ -1566,7 +1566,9 @@ int salr_load(const void* buf, int64_t buf_bytes, void* stream, salr_handle* out
 namespace {
 
 // CTAs that share a row tile's reduction (a cluster): the largest power of two up to 8 that
-// leaves all CTAs resident at once and each of them at least two chunks.
+// leaves all CTAs resident at once and each of them two chunks or more.  (Asked how many
+// clusters fit, the runtime counts one CTA to an SM for a kernel that allocates tensor memory;
+// two run.  Held to that count, up_proj M = 2048 took 28 us for t and u instead of 23.)
 int grad_cluster(int tiles, int chunks, int slots) {
   int c = 1;
   while (c < 8 && tiles * c * 2 <= slots && chunks >= 4 * c) c *= 2;

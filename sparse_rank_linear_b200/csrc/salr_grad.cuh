@@ -161,7 +161,7 @@ __device__ __forceinline__ float4 ld_cluster4(uint32_t cluster_addr) {
 // in that one CTA's chain of L2 reads: up_proj M = 2048 took 60 + 65 us for the two
 // launches.
 template <int BN>
-__global__ void __launch_bounds__(kGradThreads)
+__global__ void __launch_bounds__(kGradThreads, BN == 256 ? 1 : 2)
     grad_skinny_kernel(const __grid_constant__ GradSkinnyParams prm, const int nc,
                        const __grid_constant__ CUtensorMap ma0, const __grid_constant__ CUtensorMap mb0,
                        const __grid_constant__ CUtensorMap ma1, const __grid_constant__ CUtensorMap mb1) {
