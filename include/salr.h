@@ -39,7 +39,8 @@
  *   - Environment, read at each call: SALR_WAIT_LIMIT_CYCLES=n bounds every device wait
  *     at n SM cycles (default 2e9, about one second; failure tests lower it);
  *     SALR_FAIL_T_WAIT=1 makes the small-M kernel's readers of t wait for one part more
- *     than is ever added (failure tests only: the call then reports SALR_ERR_TIMEOUT);
+ *     than is ever added, and the 4-bit and gradient kernels wait for a copy that is never
+ *     made (failure tests only: the call then reports SALR_ERR_TIMEOUT);
  *     SALR_WIDE_MIN_ROUNDS=n sets how many full rounds of 256-row tiles the dense-scratch
  *     path needs before it uses them (default 8; tests set 0 to reach them on small
  *     shapes); SALR_TILE_GROUP_ROWS=n sets the prefill kernel's tile group (tests);

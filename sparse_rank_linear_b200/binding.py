@@ -336,8 +336,9 @@ def linear(X, weight: Weight, A_cat=None, B_cat=None, Y=None, stream=None):
         Y = X.new_empty((M, N))
     else:
         _require(Y, "Y", (M, N))
-    _check("salr_linear", load_library().salr_linear(_ptr(X), M, weight.handle, _ptr(A_cat),
-                                                     _ptr(B_cat), R, _ptr(Y), _stream_ptr(stream)))
+    with _on_device(X):
+        _check("salr_linear", load_library().salr_linear(
+            _ptr(X), M, weight.handle, _ptr(A_cat), _ptr(B_cat), R, _ptr(Y), _stream_ptr(stream)))
     return Y
 
 

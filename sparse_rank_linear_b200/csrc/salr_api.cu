@@ -601,6 +601,12 @@ void bind_call(StreamParams& sp, float* acc, uint32_t* counters, float* tacc, ui
   sp.tflag = tflags;
 }
 
+// SALR_FAIL_T_WAIT=1 (failure tests only): a wait of the kernels launched runs out.
+bool fail_wait() {
+  const char* v = getenv("SALR_FAIL_T_WAIT");
+  return v && v[0] == '1';
+}
+
 // The bound on device-side waits, in SM cycles: kWaitLimitCycles (about 1 s), or
 // SALR_WAIT_LIMIT_CYCLES (failure tests make waits run out quickly with it).  Copied to
 // the device on the call's stream whenever it differs from the value last sent there.
@@ -674,8 +680,7 @@ int launch_stream(StreamParams p, const CUtensorMap& tx, const CUtensorMap& ta,
   p.treaders = stream_t_readers(units, grid, p.kblocks, p.skew);
   // SALR_FAIL_T_WAIT=1 (failure tests only): the readers of t wait for one part more
   // than are ever added, so their bounded wait runs out and the call reports a timeout
-  const char* ft = getenv("SALR_FAIL_T_WAIT");
-  p.twant = p.tshare + (ft && ft[0] == '1' ? 1 : 0);
+  p.twant = p.tshare + (fail_wait() ? 1 : 0);
   SALR_TRY(apply_wait_limit(st));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
@@ -867,6 +872,7 @@ int launch_q4(const void* X, int M, salr_handle h, const void* A, const void* B,
   p.status = h->status;
   p.M = M;
   p.R = R;
+  p.fail = fail_wait() ? 1 : 0;
   p.records = (K + kQ4Cols - 1) / kQ4Cols;
   p.total = static_cast<long long>(blocks) * p.records;
   CUtensorMap m[3], ma, mx;
@@ -1185,6 +1191,7 @@ int salr_q4_encode(const void* W, int64_t N, int64_t K, int64_t group, int symme
 
 int salr_decode(salr_handle h, void* W_out, void* stream) {
   if (!valid_handle(h) || !W_out) return SALR_ERR_INVALID;
+  if (h->group && !on_current_device(h)) return SALR_ERR_INVALID;
   if (!aligned16(W_out)) return SALR_ERR_UNSUPPORTED;
   SALR_TRY(launch_expand(h, static_cast<uint16_t*>(W_out), static_cast<cudaStream_t>(stream)));
   return SALR_OK;
@@ -1675,6 +1682,7 @@ int salr_linear_backward(const void* dY, const void* X, int64_t M64, salr_handle
   // t and u
   GradSkinnyParams s1{}, s2{};
   s1.status = s2.status = h->status;
+  s1.fail = fail_wait() ? 1 : 0;
   GradProblem &pt = s1.p[0], &pu = s1.p[1];
   pt.tiles = want_t ? mtiles : 0;
   pt.chunks = K / 64;
@@ -1708,6 +1716,7 @@ int salr_linear_backward(const void* dY, const void* X, int64_t M64, salr_handle
   GradDxParams dx{};
   dx.dX = static_cast<uint16_t*>(dX);
   dx.status = h->status;
+  dx.fail = fail_wait() ? 1 : 0;
   dx.M = M;
   dx.K = K;
   dx.chunks = N / 64;

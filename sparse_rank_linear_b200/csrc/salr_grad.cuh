@@ -71,6 +71,15 @@ __device__ __forceinline__ bool mbar_wait_pair(uint64_t* bar, uint32_t parity) {
     if ((i & 255u) == 255u && clock64() - t0 > wait_limit()) return false;
   }
 }
+// Wait for a copy in flight on the way out after a wait that gave up: 2 ms at most (however
+// short the bound on the other waits is, copies land within microseconds, and none may land
+// in the shared memory of a CTA that has exited).
+__device__ __forceinline__ void mbar_drain(uint64_t* bar, uint32_t parity) {
+  const uint32_t a = smem_u32(bar);
+  const long long t0 = clock64();
+  while (!mbar_try_wait(a, parity) && clock64() - t0 < 4000000) {
+  }
+}
 // Tensor copy into this CTA's shared memory that reports to a barrier of either CTA.
 __device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* map, int32_t c0,
                                                  int32_t c1, uint32_t bar_cluster) {
@@ -128,6 +137,7 @@ struct GradProblem {
 struct GradSkinnyParams {
   GradProblem p[2];
   int* status;
+  int fail;  // failure tests only: the first CTA leaves out one copy, whose wait then runs out
 };
 
 struct GradCtrl {
@@ -215,7 +225,7 @@ __global__ void __launch_bounds__(kGradThreads, BN == 256 ? 1 : 2)
         if (p.a_mn) {
           tma_load_2d(a, ma, p0, r, bar);
           tma_load_2d(a + 8192, ma, p0 + 64, r, bar);
-        } else {
+        } else if (!prm.fail || blockIdx.x != 0 || c != c0) {
           tma_load_2d(a, ma, r, p0, bar);
         }
         if (p.b_mn) {
@@ -229,7 +239,7 @@ __global__ void __launch_bounds__(kGradThreads, BN == 256 ? 1 : 2)
       }
       if (*abort_flag)  // let the copies in flight land before the CTA can exit
         for (int i = issued > L::kStages ? issued - L::kStages : 0; i < issued; ++i)
-          mbar_wait(&ctrl->full[i % L::kStages], (i / L::kStages) & 1);
+          mbar_drain(&ctrl->full[i % L::kStages], (i / L::kStages) & 1);
     }
   } else if (warp == 1) {
     if (lane == 0) {
@@ -377,6 +387,7 @@ struct GradDxParams {
   int mt, kt;       // tiles of 256 tokens, of 256 columns
   int full, splits, units;  // whole tiles; parts of each later tile; units in all
   int group;        // token tiles that go together, column tile by column tile
+  int fail;         // failure tests only: the first pair leaves out one copy
 };
 
 struct GradDxUnit {
@@ -446,15 +457,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
   tc_fence_after();
   const uint32_t tmem = ctrl->tmem;
   volatile int* abort_flag = &ctrl->abort;
+  // u, and the dense weight: the u kernel ends after the expansion.  Every thread waits, so
+  // that the bounded waits below do not run while kernels ahead do.
+  griddep_wait();
+  griddep_launch_dependents();
 
   if (warp == 0) {
     if (lane == 0) {
       int s = 0, ph = 0;
       long long issued = 0;
       bool ok = true;
-      // u, and the dense weight: the u kernel ends after the expansion
-      griddep_wait();
-      griddep_launch_dependents();
       for (int u = pair; u < p.units && ok; u += pairs) {
         const GradDxUnit w = grad_dx_unit(p, u);
         const int row = w.m * 256 + static_cast<int>(rank) * 128;
@@ -473,7 +485,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
           uint8_t* b = a + 16384;
           if (c < w.nc) {
             const int n = (w.c0 + c) * kGradChunk;
-            tma_load_2d_pair(a, &mdy, n, row, bar);
+            if (!p.fail || blockIdx.x != 1 || issued != 0) tma_load_2d_pair(a, &mdy, n, row, bar);
             tma_load_2d_pair(b, &mw, col, n, bar);
             tma_load_2d_pair(b + 8192, &mw, col + 64, n, bar);
           } else {
@@ -490,7 +502,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
         // count both CTAs' bytes, and the second CTA stays until the first one is through
         if (rank == 0)
           for (long long i = issued > kDxStages ? issued - kDxStages : 0; i < issued; ++i)
-            mbar_wait_pair(&ctrl->full[i % kDxStages], (i / kDxStages) & 1);
+            mbar_drain(&ctrl->full[i % kDxStages], (i / kDxStages) & 1);
         for (int i = 0; i < 100; ++i) __nanosleep(1000);
       }
     }

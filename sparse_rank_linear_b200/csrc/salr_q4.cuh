@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(Q4TLayout<NT>::kThreads)
       }
       if (q4_aborted(ctrl))  // let the copies in flight land before the CTA can exit
         for (int i = issued > L::kStages ? issued - L::kStages : 0; i < issued; ++i)
-          mbar_wait(&ctrl->full[i % L::kStages], (i / L::kStages) & 1);
+          mbar_drain(&ctrl->full[i % L::kStages], (i / L::kStages) & 1);
     }
   } else {
     const bool live = warp * 16 < R;
@@ -325,6 +325,7 @@ struct Q4Params {
   uint32_t* count;  // [blocks][8 row tiles] arrivals, zero between calls
   int* status;
   int M, R;
+  int fail;         // failure tests only: the first CTA leaves out one copy of X
   int parts;        // > 1: clusters of so many CTAs share a row block, one part of its records each
   int records;      // of a row block
   long long total;  // records in all
@@ -430,6 +431,8 @@ __device__ __forceinline__ void q4_consume(const Q4Params& p, uint8_t* smem, Q4C
   constexpr int kRecord = 64 * kQ4Cols + kQ4Cols / GROUP * (ZEROS ? 384 : 256);  // bytes
   const int cta = blockIdx.x, ctas = gridDim.x;
   const int g = lane >> 2, tl = lane & 3, tk = q4_token(g);
+  // X comes after the kernel ahead: the bounded waits below do not run while that one does
+  if (p.R == 0) griddep_wait();
   const uint32_t mask = q4_opaque(0x000f000fu), one28 = q4_opaque(0x43004300u), eight = q4_opaque(0x43084308u);
   int s = 0, ph = 0;
   for (long long i = i0; i < i1;) {
@@ -652,11 +655,11 @@ __global__ void __launch_bounds__(Q4Layout<NT>::kThreads, Q4Layout<NT>::kPerSm)
             const uint32_t bytes = (cnt - 1) * kRecord + (at + cnt == p.records ? tail : kRecord);
             mbar_arrive_expect_tx(bar, bytes + L::kXBytes);
             bulk_g2s(dst, rec, bytes, bar);
-            if (c >= ahead) tma_load_3d(x, &mx, 0, 0, 2 * at, bar);
+            if (c >= ahead && (!p.fail || cta != 0 || issued != 0)) tma_load_3d(x, &mx, 0, 0, 2 * at, bar);
             rec += bytes;
             if (c + 1 == ahead) {  // every stage of the ring has its codes coming
               griddep_wait();
-              for (int k = 0; k < ahead; ++k)
+              for (int k = p.fail && cta == 0 ? 1 : 0; k < ahead; ++k)
                 tma_load_3d(smem + k * L::kStage, &mx, 0, 0, 2 * (c0 + k * L::kRecords), &ctrl->full[k]);
             }
           } else {
@@ -675,7 +678,7 @@ __global__ void __launch_bounds__(Q4Layout<NT>::kThreads, Q4Layout<NT>::kPerSm)
       }
       if (q4_aborted(ctrl))  // let the copies in flight land before the CTA can exit
         for (int k = issued > L::kStages ? issued - L::kStages : 0; k < issued; ++k)
-          mbar_wait(&ctrl->full[k % L::kStages], (k / L::kStages) & 1);
+          mbar_drain(&ctrl->full[k % L::kStages], (k / L::kStages) & 1);
       if (p.R > 0 && !waited) griddep_wait();  // this grid ends after the t kernel
     }
   } else {

@@ -17,6 +17,14 @@ BLOCK = 256  # elements that share a scale of the 8-bit moments
 _TYPES = {"torch.bfloat16": 0, "torch.float32": 1}
 
 
+def _held(name):
+    """Attribute for a buffer that may be changed in place (``x += y`` too) but not replaced."""
+    def put(self, value):
+        if value is not getattr(self, name):
+            raise AttributeError(f"{name[1:]} cannot be replaced: copy into it")
+    return property(lambda self: getattr(self, name), put)
+
+
 class AdamW:
     """AdamW with decoupled weight decay over ``params``, a list of contiguous CUDA tensors
     of one type (bfloat16 or float32) on one device, updated in place.
@@ -70,6 +78,7 @@ class AdamW:
         if not (math.isfinite(eps) and eps >= 0):
             raise ValueError("eps must be finite and not negative")
         self.device = first.device
+        self._kind = first.dtype
         self.lr, self.betas, self.eps, self.weight_decay = lr, (beta1, beta2), eps, weight_decay
         self.state_bits = state_bits
         self.slices, total = [], 0
@@ -77,37 +86,60 @@ class AdamW:
             self.slices.append(slice(total, total + p.numel()))
             total += -(-p.numel() // BLOCK) * BLOCK
         kind = torch.float8_e4m3fn if state_bits == 8 else torch.float32
-        self.exp_avg = torch.zeros(total, dtype=kind, device=self.device)
-        self.exp_avg_sq = torch.zeros(total, dtype=kind, device=self.device)
-        self.exp_avg_scale = self.exp_avg_sq_scale = self.master = None
+        # held for as long as the table below points into them: read-only attributes
+        m = self._exp_avg = torch.zeros(total, dtype=kind, device=self.device)
+        v = self._exp_avg_sq = torch.zeros(total, dtype=kind, device=self.device)
+        self._exp_avg_scale = self._exp_avg_sq_scale = self._master = None
         if state_bits == 8:
-            self.exp_avg_scale = torch.zeros(total // BLOCK, device=self.device)
-            self.exp_avg_sq_scale = torch.zeros(total // BLOCK, device=self.device)
+            self._exp_avg_scale = torch.zeros(total // BLOCK, device=self.device)
+            self._exp_avg_sq_scale = torch.zeros(total // BLOCK, device=self.device)
         if master:
-            self.master = torch.zeros(total, device=self.device)
+            self._master = torch.zeros(total, device=self.device)
             for p, s in zip(self.params, self.slices):
-                self.master[s].copy_(p.detach().reshape(-1))
+                self._master[s].copy_(p.detach().reshape(-1))
         self._step = torch.zeros(2, dtype=torch.int64, device=self.device)
-        self.step_count = self._step[0]
         self._numel = [p.numel() for p in self.params]
         self._table = (AdamwTensor * len(self.params))()
         for t, p, s in zip(self._table, self.params, self.slices):
-            t.param = p.data_ptr()
-            t.exp_avg = self.exp_avg.data_ptr() + s.start * self.exp_avg.element_size()
-            t.exp_avg_sq = self.exp_avg_sq.data_ptr() + s.start * self.exp_avg_sq.element_size()
+            t.exp_avg = m.data_ptr() + s.start * m.element_size()
+            t.exp_avg_sq = v.data_ptr() + s.start * v.element_size()
             if state_bits == 8:
-                t.exp_avg_scale = self.exp_avg_scale.data_ptr() + s.start // BLOCK * 4
-                t.exp_avg_sq_scale = self.exp_avg_sq_scale.data_ptr() + s.start // BLOCK * 4
+                t.exp_avg_scale = self._exp_avg_scale.data_ptr() + s.start // BLOCK * 4
+                t.exp_avg_sq_scale = self._exp_avg_sq_scale.data_ptr() + s.start // BLOCK * 4
             if master:
-                t.master = self.master.data_ptr() + s.start * 4
+                t.master = self._master.data_ptr() + s.start * 4
             t.n = p.numel()
-        # the gradients' pointers in the table, as one strided array
-        self._grads = np.frombuffer(self._table, dtype=np.uint64).reshape(len(self._table), -1)[
-            :, AdamwTensor.grad.offset // 8]
+        # columns of the table as strided arrays: every step writes both anew
+        words = np.frombuffer(self._table, dtype=np.uint64).reshape(len(self._table), -1)
+        self._grads = words[:, AdamwTensor.grad.offset // 8]
+        self._params = words[:, AdamwTensor.param.offset // 8]
         self._index = self._step.get_device()
+        self._at = None  # the parameters' addresses in the table
         self._config = AdamwConfig(beta1=beta1, beta2=beta2, eps=eps, step=self._step.data_ptr(),
                                    param_type=_TYPES[str(first.dtype)], state_bits=state_bits,
                                    master=1 if master else 0)
+
+    exp_avg = _held("_exp_avg")
+    exp_avg_sq = _held("_exp_avg_sq")
+    exp_avg_scale = _held("_exp_avg_scale")
+    exp_avg_sq_scale = _held("_exp_avg_sq_scale")
+    master = _held("_master")
+    step_count = property(lambda self: self._step[0])
+
+    def _pointers(self, tensors, numel, what):
+        """Their addresses, after checks in whole-list passes (a loop over hundreds of tensors
+        would take longer than the step), and their type (None for an empty list)."""
+        import torch
+        T = torch.Tensor
+        pointers = list(map(T.data_ptr, tensors))
+        kinds = set(map(T.dtype.__get__, tensors))
+        kind = kinds.pop() if kinds else None
+        if kinds or (kind is not None and str(kind) not in _TYPES):
+            raise TypeError(f"{what} must have one type, bfloat16 or float32")
+        if (list(map(T.numel, tensors)) != numel or not all(map(T.is_contiguous, tensors)) or
+                any(i != self._index for i in set(map(T.get_device, tensors)))):
+            raise ValueError(f"{what} must be contiguous, of the parameters' sizes and on {self.device}")
+        return pointers, kind
 
     def _scalar(self, x, name):
         import torch
@@ -123,28 +155,27 @@ class AdamW:
         ``grad_scale``: a one-element float32 CUDA tensor that multiplies every gradient (the
         factor of gradient clipping, or of undoing a loss scale)."""
         import torch
-        T = torch.Tensor
+        grads = list(grads)
         if len(grads) != len(self.params):
             raise ValueError(f"{len(grads)} gradients for {len(self.params)} params")
-        if type(grads) is not list:
-            grads = list(grads)
-        # whole-list passes: a loop over hundreds of gradients would take longer than the step
-        given = grads
         try:
-            pointers = list(map(T.data_ptr, grads))
-            numel = self._numel
-        except TypeError:  # None among them
+            pointers, kind = self._pointers(grads, self._numel, "grads")
+        except TypeError:  # None among them, or a type that fails below again
             given = [g for g in grads if g is not None]
-            pointers = [0 if g is None else g.data_ptr() for g in grads]
-            numel = [n for n, g in zip(self._numel, grads) if g is not None]
-        kinds = set(map(T.dtype.__get__, given))
-        kind = kinds.pop() if kinds else None
-        if kinds or (kind is not None and str(kind) not in _TYPES):
-            raise TypeError("grads must have one type, bfloat16 or float32")
-        if (list(map(T.numel, given)) != numel or not all(map(T.is_contiguous, given)) or
-                any(i != self._index for i in set(map(T.get_device, given)))):
-            raise ValueError(f"each gradient must be contiguous, as large as its parameter and "
-                             f"on {self.device}")
+            some, kind = self._pointers(given, [n for n, g in zip(self._numel, grads) if g is not None],
+                                        "grads")
+            some = iter(some)
+            pointers = [0 if g is None else next(some) for g in grads]
+        # the parameters may have moved since the last step (p.data = ...)
+        at = list(map(torch.Tensor.data_ptr, self.params))
+        if at != self._at:
+            at, now = self._pointers(self.params, self._numel, "params")
+            if now != self._kind:
+                raise TypeError("params must keep their type")
+            self._at = at
+            self._params[:] = at
+            # kept alive: while they are, an unchanged address means unchanged memory
+            self._kept = [p.detach() for p in self.params]
         self._grads[:] = pointers
         c = self._config
         c.grad_type = 0 if kind is None else _TYPES[str(kind)]

@@ -360,3 +360,32 @@ def test_class_refusals_on_device():
     with pytest.raises(salr.SalrError):
         opt.step([None, ok], lr=float("nan"))
     assert opt.step_count.item() == 0
+
+
+@gpu
+def test_parameters_that_moved_are_found_again():
+    p = [torch.zeros(300, device="cuda"), torch.zeros(5, device="cuda")]
+    g = [torch.ones(300, device="cuda"), torch.ones(5, device="cuda")]
+    opt = salr.AdamW(p, lr=0.1, weight_decay=0.0)
+    opt.step(g)
+    old = p[0].data
+    p[0].data = torch.full((300,), 2.0, device="cuda")
+    opt.step(g)
+    torch.cuda.synchronize()
+    assert (old == old[0]).all() and abs(old[0].item() + 0.1) < 1e-5  # one step, and left alone
+    assert ((p[0] - 1.9).abs() < 1e-5).all()
+    p[0].data = torch.zeros(299, device="cuda")
+    with pytest.raises(ValueError, match="params"):
+        opt.step(g)
+    p[0].data = torch.zeros(300, device="cuda", dtype=torch.bfloat16)
+    with pytest.raises(TypeError, match="params"):
+        opt.step(g)
+    assert opt.step_count.item() == 2
+
+
+@gpu
+def test_state_buffers_cannot_be_replaced():
+    opt = salr.AdamW([torch.zeros(3, device="cuda")], state_bits=8)
+    for name in ("exp_avg", "exp_avg_sq", "exp_avg_scale", "exp_avg_sq_scale", "master", "step_count"):
+        with pytest.raises(AttributeError):
+            setattr(opt, name, torch.zeros(256, device="cuda"))

@@ -229,3 +229,36 @@ def test_training_steps_of_the_adapters():
         opt.step([dA1, dB1, dA2, dB2])
         assert all(not torch.equal(a, b) and torch.isfinite(a).all() for a, b in zip(ads, before))
     assert opt.step_count.item() == 3
+
+
+@gpu
+def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_right(monkeypatch):
+    w, X, dY, A, B, _ = setup(384, 320, 150, 24, "bitmap")
+    monkeypatch.setenv("SALR_WAIT_LIMIT_CYCLES", "400000")  # about 0.2 ms a wait
+    monkeypatch.setenv("SALR_FAIL_T_WAIT", "1")
+    for needs in ((True, False, False), (False, True, True)):
+        salr.linear_backward(dY, X, w, A, B, needs=needs)
+        assert w.sync_status() == binding.SALR_ERR_TIMEOUT
+    monkeypatch.delenv("SALR_FAIL_T_WAIT")
+    monkeypatch.delenv("SALR_WAIT_LIMIT_CYCLES")
+    for _ in range(2):
+        check(salr.linear_backward(dY, X, w, A, B), reference(w, X, dY, A, B))
+        assert w.sync_status() == 0
+
+
+@gpu
+def test_two_calls_on_one_handle_at_a_time():
+    # the scratch is the call's own: calls on two streams do not disturb each other
+    w, X, dY, A, B, g = setup(1024, 768, 600, 32, "q4")
+    other = bf16(g, *dY.shape)
+    want = [salr.linear_backward(d, X, w, A, B) for d in (dY, other)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [None, None]
+    for _ in range(5):
+        for k, d in enumerate((dY, other)):
+            with torch.cuda.stream(streams[k]):
+                got[k] = salr.linear_backward(d, X, w, A, B)
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))

@@ -282,3 +282,48 @@ def test_calls_about_the_bitmap_form_are_refused(lib):
     p = ctypes.c_void_p
     Y = torch.empty(1, 128, dtype=torch.bfloat16, device="cuda")
     assert lib.salr_linear_noalloc(p(W.data_ptr()), 1, w.handle, p(0), p(0), 0, p(Y.data_ptr()), p(0)) == 2
+
+
+@gpu
+@pytest.mark.parametrize("N,K,M,R", [(128, 512, 3, 0), (256, 4096, 3, 0), (256, 4096, 20, 16), (4096, 1024, 1, 8)])
+def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_right(monkeypatch, N, K, M, R):
+    codes, s, z, W, g = make(N, K, 64, True)
+    w = salr.pack_q4(codes, s, z)
+    X = bf16(g, M, K)
+    A, B = (bf16(g, K, R, scale=0.05), bf16(g, R, N, scale=0.05)) if R else (None, None)
+    monkeypatch.setenv("SALR_WAIT_LIMIT_CYCLES", "400000")  # about 0.2 ms a wait
+    monkeypatch.setenv("SALR_FAIL_T_WAIT", "1")
+    salr.linear(X, w, A, B)
+    assert w.sync_status() == binding.SALR_ERR_TIMEOUT
+    monkeypatch.delenv("SALR_FAIL_T_WAIT")
+    monkeypatch.delenv("SALR_WAIT_LIMIT_CYCLES")
+    for _ in range(2):
+        check_small(salr.linear(X, w, A, B), X, W, A, B, 64)
+        assert w.sync_status() == 0
+
+
+@gpu
+@pytest.mark.parametrize("M", [1, 40])
+def test_calls_one_behind_another_see_each_others_results(M):
+    # the launches overlap at their ends: a chain through square layers must still be in order
+    ws, Ws = [], []
+    for i in range(3):
+        codes, s, z, W, g = make(512, 512, 64, i == 1, seed=i)
+        ws.append(salr.pack_q4(codes, (s.float() * 0.2).bfloat16(), z))
+        Ws.append(ws[-1].decode().double())
+    A, B = bf16(g, 512, 16, scale=0.05), bf16(g, 16, 512, scale=0.05)
+    X = bf16(g, M, 512)
+    for _ in range(20):
+        H = X
+        for i, w in enumerate(ws):
+            H = salr.linear(H, w, A if i else None, B if i else None)
+    steps, H = [], X
+    for i, w in enumerate(ws):
+        torch.cuda.synchronize()
+        H = salr.linear(H, w, A if i else None, B if i else None)
+        torch.cuda.synchronize()
+        steps.append(H)
+    H = X
+    for i, w in enumerate(ws):
+        H = salr.linear(H, w, A if i else None, B if i else None)
+    assert torch.equal(H, steps[-1])
