@@ -71,11 +71,27 @@ __device__ __forceinline__ double adam_pow(double b, long long t) {
   return r;
 }
 
-// Square root to 2^-23 (the fully rounded one takes a branch and three times the instructions).
-__device__ __forceinline__ float adam_sqrt(float x) {
-  float d;
-  asm("sqrt.approx.f32 %0, %1;" : "=f"(d) : "f"(x));
-  return d;
+// Square roots of 8 values.  The fully rounded instruction sequence branches and takes three
+// times as long as this: an approximate reciprocal root and one Newton step, which leaves all
+// but few results correctly rounded (8-bit codes next to a border then fall as those of the
+// rounded root do).  Values so small or large that the step would leave fp32's range, zero
+// among them, take the former.
+__device__ __forceinline__ void adam_sqrt8(const float (&v)[8], float (&r)[8]) {
+  float low = v[0], high = v[0];
+#pragma unroll
+  for (int k = 1; k < 8; ++k) low = fminf(low, v[k]), high = fmaxf(high, v[k]);
+  if (low >= 1e-30f && high <= 1e37f) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      float y;
+      asm("rsqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(v[k]));
+      const float s = v[k] * y;
+      r[k] = __fmaf_rn(__fmaf_rn(-s, s, v[k]), 0.5f * y, s);
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) r[k] = __fsqrt_rn(v[k]);
+  }
 }
 
 // 8 values as they lie in memory, loaded ahead of their use.
@@ -189,10 +205,14 @@ __device__ __forceinline__ float adam_warp_max_nan(float a) {
   asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(d) : "f"(a));
   return d;
 }
-__device__ __forceinline__ float adam_rcp(float x) {  // within 2^-23
-  float d;
-  asm("rcp.approx.f32 %0, %1;" : "=f"(d) : "f"(x));
-  return d;
+// a / x by an approximate reciprocal, one Newton step for it and one for the quotient, for x
+// within 2^-100 .. 1e37.
+__device__ __forceinline__ float adam_quotient(float a, float x) {
+  float y;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  y = __fmaf_rn(y, __fmaf_rn(-x, y, 1.f), y);
+  const float q = a * y;
+  return __fmaf_rn(__fmaf_rn(-x, q, a), y, q);
 }
 
 // Store x (8 values a thread, the warp's block) as e4m3 codes at element i and the block's
@@ -206,7 +226,7 @@ __device__ __forceinline__ void adam_encode(const float (&x)[8], void* codes, in
   for (int k = 1; k < 8; ++k) top = adam_max_nan(top, fabsf(x[k]));
   top = adam_warp_max_nan(top);
   const bool plain = top <= 1e37f;  // the same in every lane
-  float inv = kE4m3Max * adam_rcp(top);
+  float inv = adam_quotient(kE4m3Max, top);
   if (!plain) {  // infinite or NaN, of which the largest finite value counts, or near overflow
     top = 0.f;
 #pragma unroll
@@ -239,7 +259,7 @@ __device__ __forceinline__ void adam_encode(const float (&x)[8], void* codes, in
   }
   __stcs(reinterpret_cast<uint2*>(static_cast<uint8_t*>(codes) + i),
          make_uint2(adam_e4m3x4(y[0], y[1], y[2], y[3]), adam_e4m3x4(y[4], y[5], y[6], y[7])));
-  if (lane == 0) *sp = live ? top * (1.f / kE4m3Max) : 0.f;
+  if (lane == 0) *sp = live ? adam_quotient(top, kE4m3Max) : 0.f;
 }
 
 template <int MAXT, typename PT, typename GT, bool MASTER, bool EIGHT>
@@ -338,7 +358,10 @@ __global__ void __launch_bounds__(kAdamThreads, EIGHT ? 4 : 3)
       if (EIGHT) v[k] = __fmul_rn(v[k], v[k]);
       m[k] = __fadd_rn(__fmul_rn(m[k], b1), __fmul_rn(gk, ob1));
       v[k] = __fadd_rn(__fmul_rn(v[k], b2), __fmul_rn(__fmul_rn(gk, gk), ob2));
-      r[k] = adam_sqrt(v[k]);
+    }
+    adam_sqrt8(v, r);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
       const float step = __fdividef(m[k], __fadd_rn(__fmul_rn(r[k], root), eps));
       p[k] = __fsub_rn(__fmul_rn(p[k], decay), __fmul_rn(rate, step));
     }
