@@ -22,8 +22,10 @@
 //
 // Parts of a split reduction are added up in a fixed order: results repeat bit for bit.
 //
-// Bounds: 2 is tensor-bound (2 M N K flops); 1 and 3 read X and dY once each and are bound
-// by HBM or, when X and dY stay in L2, by L2.
+// Bounds: 2 is tensor-bound (2 M N K flops): 2.63 ms alone for N = 28672, K = 8192, M = 8192,
+// 1.46 PFLOP/s, and 3.1 to 3.4 ms in a long run under the power cap.  1 and 3 read X and dY
+// once each and are bound by HBM or, when X and dY stay in L2, by L2: 132 and 137 us for those
+// sizes (604 MB, 94 us at the copy rate).
 #pragma once
 #include <cstdint>
 #include <cuda_bf16.h>
@@ -370,7 +372,11 @@ __global__ void __launch_bounds__(kGradThreads, BN == 256 ? 1 : 2)
 // tokens of dY and its 128 columns of W per step of 64 (32 KB, half of what a lone CTA would
 // load per flop), the first CTA issues the MMAs for both, and each keeps its 128 x 256 half
 // of the accumulator in its own TMEM, twice, so that the epilogue of a tile overlaps the
-// next one.  Persistent; the tiles of a last, partial round are split along N.
+// next one.  Persistent; the tiles of a last, partial round are split along N.  Four stages:
+// with six, the pairs run further apart and meet less of each other's operands in L2, and
+// under the power cap N = 28672, K = 8192, M = 8192 took 5% longer (3.73 against 3.54 ms for
+// the whole call), while up_proj M = 2048 gained 0.7%.  Tiles go in groups of about as many
+// token tiles as column tiles: 1.08 GB of DRAM reads at 8192^3, against 2.05 without.
 constexpr int kDxStages = 4;
 constexpr int kDxStage = 32768;
 constexpr int kDxMaxParts = 4;
