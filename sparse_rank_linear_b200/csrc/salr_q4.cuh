@@ -299,11 +299,13 @@ __global__ void __launch_bounds__(Q4TLayout<NT>::kThreads)
 // otherwise each warp stores its fp32 sums and the last one to arrive for a row tile adds
 // them up in the order of the ranges: results repeat bit for bit.
 //
-// RT = 2 from 17 tokens on: a warp reads every X fragment once for its row tiles, and at 64
-// tokens one row tile a warp would read 16 bytes of X from shared memory per byte of codes.
+// RT = 2: a warp reads every X fragment once for two row tiles.  With one (twice the warps),
+// up_proj M = 24 took 21.5 against 20.4 us, large M = 16 48.0 against 45.5, and one token 1 to
+// 2% more.  Deep rings count for more than warps: at one token, three CTAs an SM of three
+// stages took 46.3 us on 28672 x 8192 where two of four stages take 37.2.
 template <int NT>
 struct Q4Layout {
-  static constexpr int RT = NT <= 2 ? 1 : 2;
+  static constexpr int RT = 2;
   static constexpr int kWarps = 8 / RT;
   static constexpr int kThreads = 32 * (kWarps + 1);
   static constexpr int kXHalf = NT * 1024;  // 8 NT tokens x 64 columns
@@ -312,7 +314,7 @@ struct Q4Layout {
   static constexpr int kRecords = NT <= 4 ? 2 : 1;
   static constexpr int kXBytes = 2 * kRecords * kXHalf;
   static constexpr int kStage = kXBytes + (kRecords * kQ4MaxRecord + 1023) / 1024 * 1024;
-  static constexpr int kStages = NT <= 4 ? 3 : 4;
+  static constexpr int kStages = NT == 4 ? 3 : 4;
   static constexpr int kSmemBytes = kStages * kStage + 1024 + 256;
   static_assert(kStages * kStage >= NT * 8 * 132 * 4, "the stages hold the sums at the end");
   // CTAs per SM that the shared memory admits (1 KB of it is the system's, per CTA)
