@@ -1587,18 +1587,29 @@ int grad_cluster(int tiles, int chunks, int slots) {
 // fp32 sums' way through L2 and the last part's adding up, about kDxSplitCost chunks' time
 // for the round.
 constexpr int kDxSplitCost = 24;
-TileSplit dx_split(int tiles, int kb, int pairs) {
+struct DxSplit {
+  int full, splits;
+  long long steps;  // of the busiest pair
+};
+DxSplit dx_split(int tiles, int kb, int pairs) {
   const int rem = tiles % pairs;
-  TileSplit r{tiles, 1};
-  long long best = kb;
+  const long long whole = static_cast<long long>(tiles / pairs) * kb;
+  DxSplit r{tiles, 1, whole + (rem ? kb : 0)};
   for (int s = 2; s <= kDxMaxParts && rem > 0 && kb / s >= 8; ++s) {
-    const long long cost = (static_cast<long long>(rem) * s + pairs - 1) / pairs * ((kb + s - 1) / s) + kDxSplitCost;
-    if (cost < best) {
-      best = cost;
-      r = TileSplit{tiles - rem, s};
-    }
+    const long long cost =
+        whole + (static_cast<long long>(rem) * s + pairs - 1) / pairs * ((kb + s - 1) / s) + kDxSplitCost;
+    if (cost < r.steps) r = DxSplit{tiles - rem, s, cost};
   }
   return r;
+}
+
+// Whether dX takes tiles of 512 columns instead of 256 (grad_dx_kernel): a step of the former
+// takes about 0.57 us against 0.39 and does twice the work, but their epilogues, about 5 us,
+// are not overlapped, and the last round may be emptier.
+bool dx_wide(int mt, int K, int kb, int pairs) {
+  const int narrow = mt * ((K + 255) / 256), wide = mt * ((K + 511) / 512);
+  const DxSplit n = dx_split(narrow, kb, pairs), w = dx_split(wide, kb, pairs);
+  return 57 * w.steps + 500ll * ((w.full + (wide - w.full) * w.splits + pairs - 1) / pairs) < 39 * n.steps;
 }
 
 template <int BN>
@@ -1632,26 +1643,27 @@ int launch_grad_skinny(const GradSkinnyParams& p, const CUtensorMap* m, bool ove
   return SALR_OK;
 }
 
+template <int HALVES>
 int launch_grad_dx(const GradDxParams& p, const CUtensorMap* m, int pairs, cudaStream_t st) {
   static std::atomic<bool> attr_set[64];  // zero-initialised: false
   int dev = 0;
   SALR_TRY(cudaGetDevice(&dev));
   if (dev < 0 || dev >= 64) return SALR_ERR_UNSUPPORTED;
   if (!attr_set[dev]) {
-    SALR_TRY(cudaFuncSetAttribute(grad_dx_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kDxSmemBytes));
+    SALR_TRY(cudaFuncSetAttribute(grad_dx_kernel<HALVES>, cudaFuncAttributeMaxDynamicSharedMemorySize, GradDx<HALVES>::kSmemBytes));
     attr_set[dev] = true;
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs));
   cfg.blockDim = dim3(kGradThreads);
-  cfg.dynamicSmemBytes = kDxSmemBytes;
+  cfg.dynamicSmemBytes = GradDx<HALVES>::kSmemBytes;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  SALR_TRY(cudaLaunchKernelEx(&cfg, grad_dx_kernel, p, m[0], m[1], m[2], m[3]));
+  SALR_TRY(cudaLaunchKernelEx(&cfg, grad_dx_kernel<HALVES>, p, m[0], m[1], m[2], m[3]));
   return SALR_OK;
 }
 
@@ -1723,20 +1735,22 @@ int salr_linear_backward(const void* dY, const void* X, int64_t M64, salr_handle
   dx.rchunks = R > 0 ? 2 * half / 64 : 0;
   dx.half = half;
   dx.mt = (M + 255) / 256;
-  dx.kt = (K + 255) / 256;
+  const bool wide = dx_wide(dx.mt, K, dx.chunks, pairs);
+  const int cols = wide ? 512 : 256;
+  dx.kt = (K + cols - 1) / cols;
   const int tiles = dx.mt * dx.kt;
-  const TileSplit ts = dx_split(tiles, dx.chunks, pairs);
+  const DxSplit ts = dx_split(tiles, dx.chunks, pairs);
   dx.full = ts.full;
   dx.splits = ts.splits;
   dx.units = dx.full + (tiles - dx.full) * dx.splits;
-  // about as many token tiles as column tiles among those in flight: the fewest operand bytes
-  dx.group = std::max(1, std::min(dx.mt, static_cast<int>(std::lround(std::sqrt(static_cast<double>(pairs))))));
+  // about as many tokens as columns among the tiles in flight: the fewest operand bytes
+  dx.group = std::max(1, std::min(dx.mt, static_cast<int>(std::lround(std::sqrt(pairs * cols / 256.0)))));
 
   // scratch, one stream-ordered allocation: [dX counts][u][t][dX fp32 parts][dense weight]
   const size_t uv = R > 0 ? round256(static_cast<size_t>(M) * 2 * half * sizeof(uint16_t)) : 0;
   const size_t split_tiles = dX ? static_cast<size_t>(tiles - dx.full) : 0;
   const size_t counts = round256(split_tiles * 8 * sizeof(uint32_t));
-  const size_t parts = split_tiles * dx.splits * 2 * 256 * 128 * sizeof(float);
+  const size_t parts = split_tiles * dx.splits * 2 * cols * 128 * sizeof(float);
   const size_t dense = dX ? static_cast<size_t>(N) * K * sizeof(uint16_t) : 0;
   uint8_t* mem = nullptr;
   SALR_TRY(dev_alloc_async(reinterpret_cast<void**>(&mem), counts + 2 * uv + parts + dense, st,
@@ -1772,7 +1786,8 @@ int salr_linear_backward(const void* dY, const void* X, int64_t M64, salr_handle
       if (!make_map(&m[0], dY, N, M, 64, 128) || !make_map(&m[1], W, K, N, 64, 64)) return SALR_ERR_CUDA;
       if (R > 0 && (!make_map(&m[2], u, 2 * half, M, 64, 128) || !make_map(&m[3], A_cat, R, K, 64, 128)))
         return SALR_ERR_CUDA;
-      rc = launch_grad_dx(dx, m, std::min(pairs, dx.units), st);
+      rc = wide ? launch_grad_dx<2>(dx, m, std::min(pairs, dx.units), st)
+                : launch_grad_dx<1>(dx, m, std::min(pairs, dx.units), st);
       if (rc != SALR_OK) return rc;
     }
     if (pa.tiles + pb.tiles > 0) {

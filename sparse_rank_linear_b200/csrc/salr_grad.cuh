@@ -368,29 +368,37 @@ __global__ void __launch_bounds__(kGradThreads, BN == 256 ? 1 : 2)
 
 // ---------------------------------------------------------------- dX
 
-// dX[M x K] in tiles of 256 tokens x 256 columns, a pair of CTAs each: a CTA loads its 128
-// tokens of dY and its 128 columns of W per step of 64 (32 KB, half of what a lone CTA would
-// load per flop), the first CTA issues the MMAs for both, and each keeps its 128 x 256 half
-// of the accumulator in its own TMEM, twice, so that the epilogue of a tile overlaps the
-// next one.  Persistent; the tiles of a last, partial round are split along N.  Four stages:
-// with six, the pairs run further apart and meet less of each other's operands in L2, and
-// under the power cap N = 28672, K = 8192, M = 8192 took 5% longer (3.73 against 3.54 ms for
-// the whole call), while up_proj M = 2048 gained 0.7%.  Tiles go in groups of about as many
-// token tiles as column tiles: 1.08 GB of DRAM reads at 8192^3, against 2.05 without.
+// dX[M x K] by pairs of CTAs (cta_group::2), in tiles of 256 tokens x 256 HALVES columns: a CTA
+// loads its 128 tokens of dY and its half of the columns of W per step of 64, the first CTA
+// issues the MMAs for both, and each keeps its 128 rows of the accumulator in its own TMEM.
+// Persistent; the tiles of a last, partial round are split along N.
+// * HALVES = 1: 32 KB a step and CTA, half of what a lone CTA would load per flop, but still
+//   bound by L2 when the clock is high (a step takes 0.39 us where the MMAs need 512 cycles).
+//   Two accumulators, so that the epilogue of a tile overlaps the next one.
+// * HALVES = 2: a quarter fewer bytes per flop (48 KB a step of 1024 cycles); one accumulator
+//   fills the TMEM, and the epilogue does not overlap.
+// Four stages: with six, the pairs run further apart and meet less of each other's operands in
+// L2, and under the power cap N = 28672, K = 8192, M = 8192 took 5% longer.  Tiles go in groups
+// of about as many tokens as columns: 1.08 GB of DRAM reads at 8192^3, against 2.05 without.
 constexpr int kDxStages = 4;
-constexpr int kDxStage = 32768;
 constexpr int kDxMaxParts = 4;
+template <int HALVES>
+struct GradDx {
+  static constexpr int kCols = 256 * HALVES;
+  static constexpr int kStage = 16384 * (1 + HALVES);
+  static constexpr int kSmemBytes = kDxStages * kStage + 1024 + 256;
+};
 
 struct GradDxParams {
   uint16_t* dX;
-  float* part;      // [split tiles][parts][2 CTAs][256 columns][128 rows]
+  float* part;      // [split tiles][parts][2 CTAs][columns of a tile][128 rows]
   uint32_t* count;  // [split tiles][2][4], zero before the launch
   int* status;
   int M, K;
   int chunks;       // N / 64
   int rchunks;      // steps of u A^T: (hi, lo) x ranks / 64, or 0
   int half;         // columns of hi in u
-  int mt, kt;       // tiles of 256 tokens, of 256 columns
+  int mt, kt;       // tiles of 256 tokens, of columns
   int full, splits, units;  // whole tiles; parts of each later tile; units in all
   int group;        // token tiles that go together, column tile by column tile
   int fail;         // failure tests only: the first pair leaves out one copy
@@ -429,16 +437,17 @@ struct GradDxCtrl {
   uint32_t tmem;
   int abort;
 };
-constexpr int kDxSmemBytes = kDxStages * kDxStage + 1024 + 256;
 
+template <int HALVES>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
     grad_dx_kernel(const __grid_constant__ GradDxParams p, const __grid_constant__ CUtensorMap mdy,
                    const __grid_constant__ CUtensorMap mw, const __grid_constant__ CUtensorMap mu,
                    const __grid_constant__ CUtensorMap ma) {
+  using L = GradDx<HALVES>;
   extern __shared__ uint8_t smem_raw[];
   // the same offset in both CTAs: dynamic shared memory starts alike in every CTA
   uint8_t* smem = align_1024(smem_raw);
-  GradDxCtrl* ctrl = reinterpret_cast<GradDxCtrl*>(smem + kDxStages * kDxStage);
+  GradDxCtrl* ctrl = reinterpret_cast<GradDxCtrl*>(smem + kDxStages * L::kStage);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
@@ -476,7 +485,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
       for (int u = pair; u < p.units && ok; u += pairs) {
         const GradDxUnit w = grad_dx_unit(p, u);
         const int row = w.m * 256 + static_cast<int>(rank) * 128;
-        const int col = w.k * 256 + static_cast<int>(rank) * 128;
+        const int col = w.k * L::kCols + static_cast<int>(rank) * 128;
         for (int c = 0; c < w.nc + w.nr; ++c) {
           if (!mbar_wait_pair(&ctrl->empty[s], ph ^ 1) || *abort_flag) {
             atomicOr(p.status, DEV_ERR_TIMEOUT);
@@ -485,19 +494,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
             break;
           }
           // both CTAs' copies count on the first CTA's barrier
-          if (rank == 0) mbar_arrive_expect_tx(&ctrl->full[s], 2 * kDxStage);
+          if (rank == 0) mbar_arrive_expect_tx(&ctrl->full[s], 2 * L::kStage);
           const uint32_t bar = map_to_rank(smem_u32(&ctrl->full[s]), 0);
-          uint8_t* a = smem + s * kDxStage;
+          uint8_t* a = smem + s * L::kStage;
           uint8_t* b = a + 16384;
           if (c < w.nc) {
             const int n = (w.c0 + c) * kGradChunk;
             if (!p.fail || blockIdx.x != 1 || issued != 0) tma_load_2d_pair(a, &mdy, n, row, bar);
-            tma_load_2d_pair(b, &mw, col, n, bar);
-            tma_load_2d_pair(b + 8192, &mw, col + 64, n, bar);
+#pragma unroll
+            for (int h = 0; h < HALVES; ++h) {
+              tma_load_2d_pair(b + h * 16384, &mw, col + h * 256, n, bar);
+              tma_load_2d_pair(b + h * 16384 + 8192, &mw, col + h * 256 + 64, n, bar);
+            }
           } else {
             const int r = (c - w.nc) * kGradChunk;
             tma_load_2d_pair(a, &mu, r, row, bar);
-            tma_load_2d_pair(b, &ma, r >= p.half ? r - p.half : r, col, bar);
+#pragma unroll
+            for (int h = 0; h < HALVES; ++h)
+              tma_load_2d_pair(b + h * 16384, &ma, r >= p.half ? r - p.half : r, col + h * 256, bar);
           }
           ++issued;
           if (++s == kDxStages) s = 0, ph ^= 1;
@@ -519,9 +533,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
       bool ok = true;
       for (int u = pair; u < p.units && ok; u += pairs, ++t) {
         const GradDxUnit w = grad_dx_unit(p, u);
-        const int b = t & 1;
+        const int b = HALVES == 1 ? t & 1 : 0;  // accumulator, and its phase
+        const uint32_t bp = HALVES == 1 ? (t >> 1) & 1 : t & 1;
         const uint32_t acc = tmem + b * 256;
-        if (!mbar_wait_pair(&ctrl->accempty[b], ((t >> 1) & 1) ^ 1) || *abort_flag) {
+        if (!mbar_wait_pair(&ctrl->accempty[b], bp ^ 1) || *abort_flag) {
           atomicOr(p.status, DEV_ERR_TIMEOUT);
           *abort_flag = 1;
           break;
@@ -535,17 +550,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
             break;
           }
           tc_fence_after();
-          const uint32_t a0 = smem_u32(smem + s * kDxStage), b0 = a0 + 16384;
+          const uint32_t a0 = smem_u32(smem + s * L::kStage), b0 = a0 + 16384;
           if (c < w.nc) {
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              mma_bf16_pair(acc, smem_desc_sw128(a0 + 32 * k, 16, 1024),
-                            smem_desc_sw128(b0 + 2048 * k, 8192, 1024), idesc_w, c != 0 || k != 0);
+#pragma unroll
+              for (int h = 0; h < HALVES; ++h)
+                mma_bf16_pair(acc + h * 256, smem_desc_sw128(a0 + 32 * k, 16, 1024),
+                              smem_desc_sw128(b0 + h * 16384 + 2048 * k, 8192, 1024), idesc_w, c != 0 || k != 0);
           } else {
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              mma_bf16_pair(acc, smem_desc_sw128(a0 + 32 * k, 16, 1024),
-                            smem_desc_sw128(b0 + 32 * k, 16, 1024), idesc_r, 1u);
+#pragma unroll
+              for (int h = 0; h < HALVES; ++h)
+                mma_bf16_pair(acc + h * 256, smem_desc_sw128(a0 + 32 * k, 16, 1024),
+                              smem_desc_sw128(b0 + h * 16384 + 32 * k, 16, 1024), idesc_r, 1u);
           }
           mma_commit_pair(&ctrl->empty[s]);
           if (++s == kDxStages) s = 0, ph ^= 1;
@@ -560,9 +579,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
     int t = 0;
     for (int u = pair; u < p.units; u += pairs, ++t) {
       const GradDxUnit w = grad_dx_unit(p, u);
-      const int b = t & 1;
+      const int b = HALVES == 1 ? t & 1 : 0;
+      const uint32_t bp = HALVES == 1 ? (t >> 1) & 1 : t & 1;
       const uint32_t tm = tmem + b * 256 + (static_cast<uint32_t>(32 * q) << 16);
-      const bool ok = mbar_wait_pair(&ctrl->accfull[b], (t >> 1) & 1) && !*abort_flag;
+      const bool ok = mbar_wait_pair(&ctrl->accfull[b], bp) && !*abort_flag;
       if (!ok) {
         atomicOr(p.status, DEV_ERR_TIMEOUT);
         *abort_flag = 1;
@@ -570,7 +590,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
       const size_t m = static_cast<size_t>(w.m) * 256 + rank * 128 + row;
-      const int k0 = w.k * 256, kn = min(256, p.K - k0);
+      const int k0 = w.k * L::kCols, kn = min(L::kCols, p.K - k0);
       uint16_t* out = p.dX + m * p.K + k0;
       const bool live = m < static_cast<size_t>(p.M);
       auto store16 = [&](int c, const float (&v)[16]) {
@@ -586,8 +606,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
           o[1] = make_uint4(h[4], h[5], h[6], h[7]);
         }
       };
-      float* parts = p.part + (static_cast<size_t>(w.st) * w.parts * 2 + rank) * 256 * 128 + row;
-      constexpr size_t kPartStride = 2 * 256 * 128;
+      float* parts = p.part + (static_cast<size_t>(w.st) * w.parts * 2 + rank) * L::kCols * 128 + row;
+      constexpr size_t kPartStride = 2 * L::kCols * 128;
       for (int c = 0; c < kn; c += 16) {
         uint32_t x[16];
         float v[16];

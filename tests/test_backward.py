@@ -103,6 +103,7 @@ def test_gradients_match_formulas(M, R):
     (4096, 4096, 2048, 96, "bitmap"),  # more tiles than CTA pairs: a last round in parts
     (1024, 8192, 1500, 128, "q4"),
     (2048, 2048, 4500, 40, "q4"),      # parts of the token reduction
+    (4096, 1472, 8100, 72, "q4"),      # tiles of 512 columns, the last of them short, some in parts
 ])
 def test_gradients_of_larger_layers(N, K, M, R, kind):
     w, X, dY, A, B, _ = setup(N, K, M, R, kind, seed=5)
