@@ -368,7 +368,8 @@ SALR_API int salr_residual_adapter(const void* W, salr_handle h, int64_t r, cons
  * once) and the rest is as described under salr_linear.  The handle must be on the current
  * device (else SALR_ERR_INVALID); its arrival counts (M <= 64) are not safe to share between
  * calls that run concurrently on different streams, captured graphs among them.  Scratch
- * (t and partial sums) is the call's own, from the library's pool.  As described for M <= 64
+ * (t, sums, the dense weight) is the call's own, from the library's pool: the first call may
+ * be a captured one, and a captured call is not touched by a later one with more tokens.  As described for M <= 64
  * under salr_linear, the call may start while the previous kernel on `stream` is still
  * running; before that has completed it reads only the handle's packed weight.
  */

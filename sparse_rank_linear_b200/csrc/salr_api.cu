@@ -131,30 +131,38 @@ cudaError_t dev_alloc(void** p, size_t bytes) {
 constexpr uint64_t kPoolKeepBytes = 1ull << 30;
 enum PoolKind { kPoolHandles = 0, kPoolScratch = 1 };
 
+cudaError_t create_pool(int dev, cudaMemPool_t* out) {
+  cudaMemPoolProps props;
+  std::memset(&props, 0, sizeof(props));
+  props.allocType = cudaMemAllocationTypePinned;
+  props.location.type = cudaMemLocationTypeDevice;
+  props.location.id = dev;
+  cudaMemPool_t pool = nullptr;
+  cudaError_t e = cudaMemPoolCreate(&pool, &props);
+  if (e != cudaSuccess) return e;
+  uint64_t keep = kPoolKeepBytes;
+  e = cudaMemPoolSetAttribute(pool, cudaMemPoolAttrReleaseThreshold, &keep);
+  if (e != cudaSuccess) {
+    cudaMemPoolDestroy(pool);
+    return e;
+  }
+  *out = pool;
+  return cudaSuccess;
+}
+
+// Both pools are made by the first call that needs one, which makes a handle: a pool cannot
+// be made while a stream is captured, and a captured call may be the first to need scratch.
 cudaError_t library_pool(int dev, PoolKind kind, cudaMemPool_t* out) {
   static std::mutex mu;
-  static cudaMemPool_t all_pools[2][64] = {};
-  cudaMemPool_t* const pools = all_pools[kind];
+  static cudaMemPool_t pools[64][2] = {};
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   std::lock_guard<std::mutex> g(mu);
-  if (!pools[dev]) {
-    cudaMemPoolProps props;
-    std::memset(&props, 0, sizeof(props));
-    props.allocType = cudaMemAllocationTypePinned;
-    props.location.type = cudaMemLocationTypeDevice;
-    props.location.id = dev;
-    cudaMemPool_t pool = nullptr;
-    cudaError_t e = cudaMemPoolCreate(&pool, &props);
+  for (cudaMemPool_t& pool : pools[dev]) {
+    if (pool) continue;
+    const cudaError_t e = create_pool(dev, &pool);
     if (e != cudaSuccess) return e;
-    uint64_t keep = kPoolKeepBytes;
-    e = cudaMemPoolSetAttribute(pool, cudaMemPoolAttrReleaseThreshold, &keep);
-    if (e != cudaSuccess) {
-      cudaMemPoolDestroy(pool);
-      return e;
-    }
-    pools[dev] = pool;
   }
-  *out = pools[dev];
+  *out = pools[dev][kind];
   return cudaSuccess;
 }
 
@@ -769,7 +777,10 @@ int cluster_room(ClusterRoom& c, Kernel kern, int threads, int smem, int dev, in
       cfg.attrs = attr;
       cfg.numAttrs = 1;
       int n = 0;
-      if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) n = 0;
+      if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
+        cudaGetLastError();  // no clusters for this call; the next one asks again
+        return 0;
+      }
       c.room[dev][k] = n;
     }
     c.known[dev] = 1;
@@ -1298,12 +1309,44 @@ int salr_linear(const void* X, int64_t M, salr_handle h, const void* A_cat, cons
   pp.cbuf = static_cast<int>((h->max16 * 16 + 32 + 1023) / 1024 * 1024);
   pp.full = pl.full;
   pp.splits = pl.splits;
-  if (pp.splits > 1) {
-    const size_t ntail = static_cast<size_t>(pl.tiles - pl.full);
-    rc = ensure_workspace(h, ntail * pl.rows * bnt, ntail * 4, st);
-    if (rc != SALR_OK) return rc;
-    pp.acc = h->work.ws;
-    pp.counters = h->work.counters;
+  // t and the split sums: a bitmap handle keeps them (zero between calls); a 4-bit handle's
+  // calls take them from the library pool, beside the dense weight, so that a captured call
+  // holds its own and a later call with more tokens cannot move them.
+  const size_t ntail = pp.splits > 1 ? static_cast<size_t>(pl.tiles - pl.full) : 0;
+  const size_t sums = ntail * pl.rows * bnt;
+  TScratch t{};
+  uint8_t* mem = nullptr;
+  uint8_t* wdense = nullptr;
+  auto done = [&](int code) {
+    if (mem) cudaFreeAsync(mem, st);
+    return code;
+  };
+  if (h->group) {
+    const size_t rows = R > 0 ? static_cast<size_t>((M + 255) / 256 * 256) : 0;
+    const size_t tb = rows * 128 * sizeof(uint16_t), t32b = rows * 128 * sizeof(float);
+    const size_t zeroed = tb + t32b + sums * sizeof(float) + (rows / 32 + ntail * 4) * sizeof(uint32_t);
+    const size_t dense = pl.path == 2 ? static_cast<size_t>(h->N) * h->K * 2 : 0;
+    SALR_TRY(dev_alloc_async(reinterpret_cast<void**>(&mem), round256(zeroed) + dense, st, kPoolScratch));
+    t.T = reinterpret_cast<uint16_t*>(mem);
+    t.T32 = reinterpret_cast<float*>(mem + tb);
+    pp.acc = t.T32 + rows * 128;
+    t.counters = reinterpret_cast<uint32_t*>(pp.acc + sums);
+    pp.counters = t.counters + rows / 32;
+    wdense = mem + round256(zeroed);
+    const cudaError_t e = zeroed ? cudaMemsetAsync(mem, 0, zeroed, st) : cudaSuccess;
+    if (e != cudaSuccess) return done(cuda_status(e));
+  } else {
+    if (pp.splits > 1) {
+      rc = ensure_workspace(h, sums, ntail * 4, st);
+      if (rc != SALR_OK) return rc;
+      pp.acc = h->work.ws;
+      pp.counters = h->work.counters;
+    }
+    if (pl.path == 2) {
+      SALR_TRY(dev_alloc_async(reinterpret_cast<void**>(&mem), static_cast<size_t>(h->N) * h->K * 2, st,
+                               kPoolScratch));
+      wdense = mem;
+    }
   }
   // persistent: at most one CTA per SM, each taking units cta, cta + grid, ...
   pp.units = pl.units;
@@ -1314,37 +1357,29 @@ int salr_linear(const void* X, int64_t M, salr_handle h, const void* A_cat, cons
   // there by TMA.
   CUtensorMap tw;
   std::memset(&tw, 0, sizeof(tw));
-  uint8_t* wdense = nullptr;
   pp.dense = pl.path == 2 ? 1 : 0;
   pp.wide = pl.rows == 256 ? 1 : 0;
   pp.rtiles = static_cast<int>(h->N / pl.rows);
   pp.group_rows = pl.group_rows;
   if (pp.dense) {
-    const cudaError_t e =
-        dev_alloc_async(reinterpret_cast<void**>(&wdense), static_cast<size_t>(h->N) * h->K * 2, st,
-                        kPoolScratch);
-    if (e != cudaSuccess) return cuda_status(e);
     const cudaError_t le = launch_expand(h, reinterpret_cast<uint16_t*>(wdense), st);
-    if (le != cudaSuccess || !make_map(&tw, wdense, h->K, h->N, 64, 128)) {
-      cudaFreeAsync(wdense, st);
-      return le != cudaSuccess ? cuda_status(le) : SALR_ERR_CUDA;
-    }
+    if (le != cudaSuccess || !make_map(&tw, wdense, h->K, h->N, 64, 128))
+      return done(le != cudaSuccess ? cuda_status(le) : SALR_ERR_CUDA);
   }
-  auto release_dense = [&](int code) {
-    if (wdense) cudaFreeAsync(wdense, st);
-    return code;
-  };
   if (R > 0) {
-    rc = ensure_tscratch(h, M, st);
-    if (rc != SALR_OK) return release_dense(rc);
-    if (!make_map(&ta, A_cat, R, h->K, 64, 64)) return release_dense(SALR_ERR_CUDA);
+    if (!h->group) {
+      rc = ensure_tscratch(h, M, st);
+      if (rc != SALR_OK) return done(rc);
+      t = h->tscr;
+    }
+    if (!make_map(&ta, A_cat, R, h->K, 64, 64)) return done(SALR_ERR_CUDA);
     // B_cat^T in chunks of 64 ranks (ranks past R read as zero)
-    if (!make_map(&tb, B_cat, h->N, R, 64, 64)) return release_dense(SALR_ERR_CUDA);
-    if (!make_map(&tt, h->tscr.T, 128, M, 64, bnt)) return release_dense(SALR_ERR_CUDA);
+    if (!make_map(&tb, B_cat, h->N, R, 64, 64)) return done(SALR_ERR_CUDA);
+    if (!make_map(&tt, t.T, 128, M, 64, bnt)) return done(SALR_ERR_CUDA);
     TParams tp{};
-    tp.T = h->tscr.T;
-    tp.T32 = h->tscr.T32;
-    tp.counters = h->tscr.counters;
+    tp.T = t.T;
+    tp.T32 = t.T32;
+    tp.counters = t.counters;
     tp.status = h->status;
     tp.M = static_cast<int>(M);
     tp.R16 = R16;
@@ -1359,12 +1394,12 @@ int salr_linear(const void* X, int64_t M, salr_handle h, const void* A_cat, cons
     tp.splits = std::max(1, std::min(KB / 4, free_sms / TT));
     rc = bnt == 128 ? launch_t<128>(tp, tx, ta, TT * tp.splits, st)
                     : launch_t<256>(tp, tx, ta, TT * tp.splits, st);
-    if (rc != SALR_OK) return release_dense(rc);
+    if (rc != SALR_OK) return done(rc);
   }
   rc = bnt == 128  ? launch_prefill<128, false>(pp, tx, tb, tt, tw, grid, R > 0, st)
        : pp.wide    ? launch_prefill<256, true>(pp, tx, tb, tt, tw, grid, R > 0, st)
                     : launch_prefill<256, false>(pp, tx, tb, tt, tw, grid, R > 0, st);
-  return release_dense(rc);
+  return done(rc);
 }
 
 int salr_linear_host(const void* X_host, int64_t M, salr_handle h, const void* A_cat,

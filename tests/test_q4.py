@@ -236,19 +236,21 @@ def test_infinite_activation_gives_the_formulas_infinities():
 
 
 @gpu
-def test_captured_calls_and_another_stream():
-    codes, s, z, W, g = make(256, 1024, 64, True)
+@pytest.mark.parametrize("N,K", [(256, 1024), (384, 512), (128, 192)])  # clusters, ranges, one range
+@pytest.mark.parametrize("R", [0, 32])
+def test_captured_calls_and_another_stream(N, K, R):
+    codes, s, z, W, g = make(N, K, 64, True)
     w = salr.pack_q4(codes, s, z)
-    A, B = bf16(g, 1024, 32, scale=0.05), bf16(g, 32, 256, scale=0.05)
-    X = bf16(g, 5, 1024)
-    Y = torch.empty(5, 256, dtype=torch.bfloat16, device="cuda")
+    A, B = (bf16(g, K, R, scale=0.05), bf16(g, R, N, scale=0.05)) if R else (None, None)
+    X = bf16(g, 5, K)
+    Y = torch.empty(5, N, dtype=torch.bfloat16, device="cuda")
     graph = torch.cuda.CUDAGraph()
     side = torch.cuda.Stream()
     with torch.cuda.graph(graph, stream=side):
         salr.linear(X, w, A, B, Y=Y)
         salr.linear(X, w, A, B, Y=Y)
     for k in range(3):
-        X.copy_(bf16(g, 5, 1024))
+        X.copy_(bf16(g, 5, K))
         graph.replay()
         torch.cuda.synchronize()
         check_small(Y, X, W, A, B, 64)
@@ -256,7 +258,7 @@ def test_captured_calls_and_another_stream():
     Z = torch.empty_like(Y)
     salr.linear(X, w, A, B, Y=Z, stream=side)
     side.synchronize()
-    assert torch.equal(Y, Z)
+    assert torch.equal(Y, Z) and w.sync_status() == 0
 
 
 @gpu
