@@ -22,8 +22,8 @@
 //
 // Parts of a split reduction are added up in a fixed order: results repeat bit for bit.
 //
-// Bounds: 2 is tensor-bound (2 M N K flops): 2.63 ms alone for N = 28672, K = 8192, M = 8192,
-// 1.46 PFLOP/s, and 3.1 to 3.4 ms in a long run under the power cap.  1 and 3 read X and dY
+// Bounds: 2 is tensor-bound (2 M N K flops): 2.44 ms alone for N = 28672, K =
+// 8192, M = 8192, 1.58 PFLOP/s, and 2.93 in a long run under the power cap.  1 and 3 read X and dY
 // once each and are bound by HBM or, when X and dY stay in L2, by L2: 132 and 137 us for those
 // sizes (604 MB, 94 us at the copy rate).
 #pragma once

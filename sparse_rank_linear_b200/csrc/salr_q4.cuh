@@ -26,13 +26,13 @@
 // Bound: HBM, by the codes (0.5 byte per weight plus scales), in the limit.  At the copy rate
 // an SM has 46 weights to rebuild per cycle; the rebuild is 0.9 instructions per weight on the
 // integer pipe (half of the issue rate), at most 73 weights per cycle, and with the products,
-// the scaling and the stages' handshake measured 28 at M = 1 on 28672 x 8192 (38.8 us, 3.4
+// the scaling and the stages' handshake measured 23 at M = 1 on 28672 x 8192 (35.9 us, 3.5
 // TB/s).  m16n8k16 takes 8 cycles per scheduler, so from about 20 tokens on the products set
-// the floor: 1024 / M weights per cycle.  The legacy products are the choice because they take
+// the floor: 1024 / M weights per cycle; measured half of that (large M = 64: 121 us).  The legacy products are the choice because they take
 // the rebuilt weights from registers and give each group's sum back in registers, where its
 // fp32 scale is one multiply-add; in tensor memory, the scale would have to be rounded into
 // the bf16 weights.  Short calls are bound by latencies (launch, first copy 2 us, sums over a
-// cluster 2 us): 6.9 us for 4096 x 4096 at M = 1, its bytes' time being 1.4.
+// cluster 2 us): 5.9 us for 4096 x 4096 at M = 1, its bytes' time being 1.4.
 #pragma once
 #include <cstdint>
 #include <cuda_bf16.h>
