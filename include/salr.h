@@ -347,11 +347,13 @@ SALR_API int salr_residual_adapter(const void* W, salr_handle h, int64_t r, cons
  * salr_linear_backward, salr_decode, salr_info (nnz = N K; bytes = codes, scales and zero
  * points), salr_sync_status and salr_free.  Calls that are about the bitmap form
  * (salr_format_view, salr_save_size, salr_save, salr_residual_adapter) and
- * salr_linear_noalloc return SALR_ERR_UNSUPPORTED for it.
+ * salr_linear_noalloc return SALR_ERR_UNSUPPORTED for it.  salr_linear_plan describes calls
+ * on bitmap weights.
  *
  * codes    device, 16-byte aligned, N x K / 2 bytes: q[n, 2i] in the low and q[n, 2i + 1]
  *          in the high nibble of byte i of row n.
- * scales   device, N x (K / group) bf16.
+ * scales   device, N x (K / group) bf16.  A value that is not finite makes the call fail
+ *          with SALR_ERR_INVALID.
  * zeros    device, N x (K / group) bytes, or NULL for 8 everywhere.  A value above 15
  *          makes the call fail with SALR_ERR_INVALID.
  * group    32, 64 or 128; K must be a multiple of it (else SALR_ERR_UNSUPPORTED).
@@ -362,9 +364,10 @@ SALR_API int salr_residual_adapter(const void* W, salr_handle h, int64_t r, cons
  * The arrays may be freed once the call returns; it synchronises `stream` once.
  *
  * salr_linear on such a handle: for M <= 64 the codes are rebuilt in registers (q - z
- * exactly, in bf16), products and sums are fp32, each group's sum is scaled in fp32, t =
- * X A_cat is kept as two bf16 parts (16 bits of significand), and results repeat bit for bit.  Two kernels with adapters, one
- * without.  Above that, the weight is expanded to a dense bf16 scratch (s (q - z) rounded
+ * exactly, in bf16), products and sums are fp32, each group's sum is scaled in fp32 (so a
+ * group's sum of (q - z) X must stay finite before it is scaled: |X| up to 2^116 is safe), t =
+ * X A_cat is kept as two bf16 parts (16 bits of significand), and results repeat bit for bit.
+ * Two kernels with adapters, one without.  Above that, the weight is expanded to a dense bf16 scratch (s (q - z) rounded
  * once) and the rest is as described under salr_linear.  The handle must be on the current
  * device (else SALR_ERR_INVALID); its arrival counts (M <= 64) are not safe to share between
  * calls that run concurrently on different streams, captured graphs among them.  Scratch

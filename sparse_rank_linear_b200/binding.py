@@ -133,7 +133,8 @@ def _ptr(t):
     return t.data_ptr() if t is not None else 0
 
 
-def _require(t, name, shape=None, device=True):
+def _require(t, name, shape=None, device=True, beside=None):
+    """Checks of a bf16 tensor; ``beside``: a CUDA tensor on whose device it has to be."""
     import torch
     if t.dtype != torch.bfloat16:
         raise TypeError(f"{name} must be bfloat16")
@@ -141,6 +142,8 @@ def _require(t, name, shape=None, device=True):
         raise ValueError(f"{name} must be contiguous (row-major)")
     if device and not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
+    if beside is not None and t.get_device() != beside.get_device():
+        raise ValueError(f"{name} must be on {beside.device}")
     if shape is not None and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
@@ -330,12 +333,12 @@ def linear(X, weight: Weight, A_cat=None, B_cat=None, Y=None, stream=None):
     R = 0
     if A_cat is not None:
         R = A_cat.shape[1]
-        _require(A_cat, "A_cat", (K, R))
-        _require(B_cat, "B_cat", (R, N))
+        _require(A_cat, "A_cat", (K, R), beside=X)
+        _require(B_cat, "B_cat", (R, N), beside=X)
     if Y is None:
         Y = X.new_empty((M, N))
     else:
-        _require(Y, "Y", (M, N))
+        _require(Y, "Y", (M, N), beside=X)
     with _on_device(X):
         _check("salr_linear", load_library().salr_linear(
             _ptr(X), M, weight.handle, _ptr(A_cat), _ptr(B_cat), R, _ptr(Y), _stream_ptr(stream)))
@@ -355,15 +358,17 @@ def linear_backward(dY, X, weight: Weight, A_cat=None, B_cat=None, dX=None, dA=N
     R = 0
     if A_cat is not None:
         R = A_cat.shape[1]
-        _require(A_cat, "A_cat", (K, R))
-        _require(B_cat, "B_cat", (R, N))
+        _require(A_cat, "A_cat", (K, R), beside=dY)
+        _require(B_cat, "B_cat", (R, N), beside=dY)
     want_x, want_a, want_b = bool(needs[0]), bool(needs[1]) and R > 0, bool(needs[2]) and R > 0
     if not (want_x or want_a or want_b):
         raise ValueError("no gradient is wanted")
     if want_a or want_b:
         if X is None:
             raise ValueError("X is needed for dA and dB")
-        _require(X, "X", (M, K))
+        _require(X, "X", (M, K), beside=dY)
+    else:
+        X = None
     out = []
     for want, t, name, shape in ((want_x, dX, "dX", (M, K)), (want_a, dA, "dA", (K, R)),
                                  (want_b, dB, "dB", (R, N))):
@@ -372,7 +377,7 @@ def linear_backward(dY, X, weight: Weight, A_cat=None, B_cat=None, dX=None, dA=N
         elif t is None:
             t = dY.new_empty(shape)
         else:
-            _require(t, name, shape)
+            _require(t, name, shape, beside=dY)
         out.append(t)
     dX, dA, dB = out
     with _on_device(dY):

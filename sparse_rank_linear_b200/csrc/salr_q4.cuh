@@ -760,8 +760,11 @@ __global__ void __launch_bounds__(256)
       const int pair = word % 64, grp = (col % kQ4Cols) / w.group;
       const long long r0 = block * 128ll + pair / 8 * 16 + pair % 8, at = r0 * groups + col / w.group;
       const long long at8 = at + 8ll * groups;
-      reinterpret_cast<uint32_t*>(rec + 64 * cols)[grp * 64 + pair] =
-          scales[at] | static_cast<uint32_t>(scales[at8]) << 16;
+      const uint32_t s0 = scales[at], s1 = scales[at8];
+      // a scale that is not finite is refused: applied to a group's sum, it would not give
+      // the infinities and NaN of its single products
+      if ((s0 & 0x7f80u) == 0x7f80u || (s1 & 0x7f80u) == 0x7f80u) atomicOr(status, DEV_ERR_FORMAT);
+      reinterpret_cast<uint32_t*>(rec + 64 * cols)[grp * 64 + pair] = s0 | s1 << 16;
       if (zeros) {
         const uint32_t z0 = zeros[at], z1 = zeros[at8];
         if (z0 > 15 || z1 > 15) atomicOr(status, DEV_ERR_FORMAT);

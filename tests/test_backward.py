@@ -183,6 +183,16 @@ def test_captured_call_beside_an_eager_one():
 
 
 @gpu
+def test_input_that_is_not_needed_is_not_looked_at():
+    w, X, dY, A, B, _ = setup(128, 192, 40, 8, "q4")
+    odd = torch.empty(40 * 192 + 1, dtype=torch.bfloat16, device="cuda")[1:].view(40, 192)
+    want = salr.linear_backward(dY, X, w, A, B)[0]
+    for x in (odd, X.cpu(), None):
+        got = salr.linear_backward(dY, x, w, A, B, needs=(True, False, False))
+        assert torch.equal(got[0], want) and got[1] is None and got[2] is None
+
+
+@gpu
 def test_refusals_on_device(lib):
     w, X, dY, A, B, _ = setup(128, 128, 4, 8, "q4")
     P = ctypes.c_void_p

@@ -52,6 +52,40 @@ def test_python_checks():
         salr.encode_q4(torch.zeros(128, 128, dtype=torch.bfloat16))
 
 
+class Elsewhere:
+    """What the checks look at, of a bf16 CUDA tensor on a given device."""
+    dtype, is_cuda = torch.bfloat16, True
+
+    def __init__(self, shape, index):
+        self.shape, self.index, self.device = shape, index, f"cuda:{index}"
+
+    def dim(self):
+        return len(self.shape)
+
+    def is_contiguous(self):
+        return True
+
+    def get_device(self):
+        return self.index
+
+
+class Square:
+    def _shape(self):
+        return 128, 128
+
+
+def test_tensors_of_another_device_are_refused():
+    X, Y, A, B = (Elsewhere(s, i) for s, i in (((4, 128), 0), ((4, 128), 1), ((128, 8), 0), ((8, 128), 0)))
+    far = [Elsewhere(t.shape, 1) for t in (A, B)]
+    for a, b, y, name in ((far[0], B, None, "A_cat"), (A, far[1], None, "B_cat"), (A, B, Y, "Y")):
+        with pytest.raises(ValueError, match=f"{name} must be on cuda:0"):
+            salr.linear(X, Square(), a, b, Y=y)
+    for x, a, b, dx, name in ((Y, A, B, None, "X"), (X, far[0], B, None, "A_cat"), (X, A, far[1], None, "B_cat"),
+                              (X, A, B, Y, "dX")):
+        with pytest.raises(ValueError, match=f"{name} must be on cuda:0"):
+            salr.linear_backward(X, x, Square(), a, b, dX=dx)
+
+
 # ---------------------------------------------------------------- helpers
 
 
@@ -116,6 +150,15 @@ def test_pack_and_decode(N, K, group, zeros):
 def test_zero_point_above_15_is_refused():
     codes, s, z, _, _ = make(128, 128, 64, True)
     z[77, 1] = 16
+    with pytest.raises(salr.SalrError, match="INVALID"):
+        salr.pack_q4(codes, s, z)
+
+
+@gpu
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+def test_scale_that_is_not_finite_is_refused(bad):
+    codes, s, z, _, _ = make(256, 128, 32, True)
+    s[200, 3] = bad
     with pytest.raises(salr.SalrError, match="INVALID"):
         salr.pack_q4(codes, s, z)
 
