@@ -190,7 +190,6 @@ __global__ void __launch_bounds__(kGradThreads, BN == 256 ? 1 : 2)
   const int c0 = static_cast<int>(static_cast<long long>(part) * p.chunks / nc);
   const int c1 = static_cast<int>(static_cast<long long>(part + 1) * p.chunks / nc);
   const int p0 = tile * 128;
-  griddep_launch_dependents();
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < L::kStages; ++s) {
@@ -205,6 +204,9 @@ __global__ void __launch_bounds__(kGradThreads, BN == 256 ? 1 : 2)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  // Only once this CTA holds its tensor memory: a CTA of the next kernel that came to this SM
+  // first could take all of it, and then wait for this grid, which would wait for it.
+  griddep_launch_dependents();
   const uint32_t tmem = ctrl->tmem;
   volatile int* abort_flag = &ctrl->abort;
 

@@ -684,8 +684,6 @@ __global__ void __launch_bounds__(kTThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   TCtrl* ctrl = reinterpret_cast<TCtrl*>(smem + kTStages * L::kStage);
-  // the layer kernel that follows may start now: it waits for this grid before reading t
-  griddep_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int j = blockIdx.x % p.TT, sidx = blockIdx.x / p.TT;
   const int kb0 = static_cast<int>(static_cast<long long>(sidx) * p.kblocks / p.splits);
@@ -705,6 +703,9 @@ __global__ void __launch_bounds__(kTThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  // The layer kernel that follows may start now (it waits for this grid before reading t):
+  // not before this CTA holds its tensor memory, of which that kernel takes all.
+  griddep_launch_dependents();
   const uint32_t tmem = ctrl->tmem;
   volatile int* abort_flag = &ctrl->abort;
 

@@ -197,7 +197,6 @@ __global__ void __launch_bounds__(32 * (kStreamFixedWarps + NDEC + kStreamGroups
   StreamCtrl* ctrl = reinterpret_cast<StreamCtrl*>(bcbuf + p.bcbuf);
   uint2* ntab = reinterpret_cast<uint2*>(bcbuf + p.bcbuf + kStreamCtrlBytes);  // 16 x 8 B, 1 KB aligned
 
-  griddep_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const bool adapter = p.R > 0;
   const int G = gridDim.x, cta = blockIdx.x;
@@ -269,6 +268,8 @@ __global__ void __launch_bounds__(32 * (kStreamFixedWarps + NDEC + kStreamGroups
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  // not before this CTA holds its tensor memory, of which the next kernel may take all
+  griddep_launch_dependents();
   const uint32_t tmem = ctrl->tmem;
   const uint32_t tmem_ts = tmem + 2 * BNT;  // t^T share accumulator [128 ranks x BNT]
   const uint32_t tmem_a = tmem + L::a_col();  // rebuilt-block ring, 32 columns per slot
