@@ -367,14 +367,16 @@ SALR_API int salr_residual_adapter(const void* W, salr_handle h, int64_t r, cons
  * exactly, in bf16), products and sums are fp32, each group's sum is scaled in fp32 (so a
  * group's sum of (q - z) X must stay finite before it is scaled: |X| up to 2^116 is safe), t =
  * X A_cat is kept as two bf16 parts (16 bits of significand), and results repeat bit for bit.
- * Two kernels with adapters, one without.  Above that, the weight is expanded to a dense bf16 scratch (s (q - z) rounded
- * once) and the rest is as described under salr_linear.  The handle must be on the current
- * device (else SALR_ERR_INVALID); its arrival counts (M <= 64) are not safe to share between
- * calls that run concurrently on different streams, captured graphs among them.  Scratch
- * (t, sums, the dense weight) is the call's own, from the library's pool: the first call may
- * be a captured one, and a captured call is not touched by a later one with more tokens.  As described for M <= 64
- * under salr_linear, the call may start while the previous kernel on `stream` is still
- * running; before that has completed it reads only the handle's packed weight.
+ * One kernel, one more with adapters, and one more where row blocks are shared by CTAs whose
+ * sums meet in memory.  Above that, the weight is expanded to a dense bf16 scratch (s (q - z)
+ * rounded once) and the rest is as described under salr_linear.  The handle must be on the
+ * current device (else SALR_ERR_INVALID).  Scratch (t, sums, the dense weight) is the call's
+ * own, from the library's pool, whatever M is: calls on one handle may run concurrently on
+ * different streams, captured graphs among them; the first call may be a captured one, and a
+ * captured call is not touched by a later one with more tokens.  (salr_linear_host still
+ * stages X and Y in the handle.)  As described for M <= 64 under salr_linear, the call may
+ * start while the previous kernel on `stream` is still running; before that has completed it
+ * reads only the handle's packed weight.
  */
 SALR_API int salr_q4_pack(const void* codes, const void* scales, const void* zeros, int64_t N,
                           int64_t K, int64_t group, void* stream, salr_handle* out);

@@ -325,8 +325,8 @@ def residual_adapter(W, weight: Weight, r: int, q: int = 2, oversample: int = 16
 
 def linear(X, weight: Weight, A_cat=None, B_cat=None, Y=None, stream=None):
     """salr_linear: Y = X (M.W)^T + (X A_cat) B_cat; returns Y (M x N bf16).  Calls on one
-    weight share workspace that it holds, so they must not run at the same time on different
-    streams (the weight of one layer is applied once at a time)."""
+    bitmap weight share workspace that it holds, so they must not run at the same time on
+    different streams; calls on one 4-bit weight may."""
     N, K = weight._shape()
     _require(X, "X")
     M = X.shape[0]

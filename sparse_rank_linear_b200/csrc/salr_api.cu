@@ -96,7 +96,6 @@ struct salr_weight_s {
   size_t y_cap;
   int group;     // 4-bit weights: columns per scale; 0: bitmap weight
   Q4View q4;     // 4-bit weights: the packed codes, scales and zero points, in mem
-  uint32_t* q4_count;  // 4-bit weights: the small-M kernel's arrival counts, 8 a row block, in mem
 };
 
 namespace {
@@ -838,6 +837,13 @@ int launch_q4_kernel(Q4Params p, const CUtensorMap* m, F&& t_first, cudaStream_t
   cfg.numAttrs = p.parts > 1 ? 2 : 1;
   int rc = t_first();
   if (rc == SALR_OK) rc = cuda_status(cudaLaunchKernelEx(&cfg, kern, p, m[0], m[1], m[2]));
+  if (rc == SALR_OK && meet) {
+    Q4SumParams s{p.part, p.Y, p.M, p.w.N, p.records, ctas, p.total};
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks), static_cast<unsigned>((p.M + kQ4SumWarps - 1) / kQ4SumWarps));
+    cfg.blockDim = dim3(32 * kQ4SumWarps);
+    cfg.dynamicSmemBytes = 0;
+    rc = cuda_status(cudaLaunchKernelEx(&cfg, q4_sum_kernel, s));  // numAttrs is 1: no cluster
+  }
   const cudaError_t f = sums ? cudaFreeAsync(sums, st) : cudaSuccess;
   return rc != SALR_OK ? rc : cuda_status(f);
 }
@@ -879,7 +885,6 @@ int launch_q4(const void* X, int M, salr_handle h, const void* A, const void* B,
   Q4Params p{};
   p.w = h->q4;
   p.Y = static_cast<uint16_t*>(Y);
-  p.count = h->q4_count;
   p.status = h->status;
   p.M = M;
   p.R = R;
@@ -1086,8 +1091,6 @@ int salr_encode(const void* W, int64_t N, int64_t K, float sparsity, void* strea
 
 namespace {
 
-size_t q4_count_bytes(const salr_weight_s* h) { return static_cast<size_t>(h->N / 128) * 8 * sizeof(uint32_t); }
-
 bool valid_group(int64_t K, int64_t group) {
   return (group == 32 || group == 64 || group == 128) && K % group == 0;
 }
@@ -1128,13 +1131,9 @@ int q4_make(const void* codes, const void* scales, const void* zeros, int64_t N,
     return code;
   };
   cudaError_t e;
-  const size_t data = round256(h->blob_bytes), cb = q4_count_bytes(h);
-  if ((e = alloc_handle_memory(h, data + cb, st)) != cudaSuccess) return fail(cuda_status(e));
+  if ((e = alloc_handle_memory(h, round256(h->blob_bytes), st)) != cudaSuccess) return fail(cuda_status(e));
   h->q4.data = h->blob;
-  h->q4_count = reinterpret_cast<uint32_t*>(h->blob + data);
-  if ((e = cudaMemsetAsync(h->status, 0, sizeof(int), st)) != cudaSuccess ||
-      (e = cudaMemsetAsync(h->q4_count, 0, cb, st)) != cudaSuccess)
-    return fail(cuda_status(e));
+  if ((e = cudaMemsetAsync(h->status, 0, sizeof(int), st)) != cudaSuccess) return fail(cuda_status(e));
   const long long words = N / 128 * (K / 64) * 1024;
   const unsigned grid = static_cast<unsigned>(std::min<long long>((words + 255) / 256, 16ll * device_sms(h->device)));
   q4_pack_kernel<<<grid, 256, 0, st>>>(static_cast<const uint32_t*>(codes), static_cast<const uint16_t*>(scales),
@@ -2062,7 +2061,6 @@ int salr_sync_status(salr_handle h, void* stream) {
     SALR_TRY(cudaMemset(h->sscr.tacc, 0, kTBuf * sizeof(float)));
     SALR_TRY(cudaMemset(h->sscr.tflags, 0, 2 * sizeof(uint32_t)));
   }
-  if (h->q4_count) SALR_TRY(cudaMemset(h->q4_count, 0, q4_count_bytes(h)));
   const int nrc = noalloc_reset(h->device);
   if (nrc != SALR_OK) return nrc;
   if (status & DEV_ERR_TIMEOUT) return SALR_ERR_TIMEOUT;

@@ -26,7 +26,7 @@
 // Bound: HBM, by the codes (0.5 byte per weight plus scales), in the limit.  At the copy rate
 // an SM has 46 weights to rebuild per cycle; the rebuild is 0.9 instructions per weight on the
 // integer pipe (half of the issue rate), at most 73 weights per cycle, and with the products,
-// the scaling and the stages' handshake measured 23 at M = 1 on 28672 x 8192 (35.9 us, 3.5
+// the scaling and the stages' handshake measured 24 at M = 1 on 28672 x 8192 (34.1 us, 3.9
 // TB/s).  m16n8k16 takes 8 cycles per scheduler, so from about 20 tokens on the products set
 // the floor: 1024 / M weights per cycle; measured half of that (large M = 64: 121 us).  The legacy products are the choice because they take
 // the rebuilt weights from registers and give each group's sum back in registers, where its
@@ -296,8 +296,8 @@ __global__ void __launch_bounds__(Q4TLayout<NT>::kThreads)
 // registers and multiply.  The CTA whose range holds a row block's first record also takes
 // the block's adapter, after its weight stages: 32 ranks a stage, B by TMA, read
 // transposed, t in its two parts.  A block that lies in one range is written at once;
-// otherwise each warp stores its fp32 sums and the last one to arrive for a row tile adds
-// them up in the order of the ranges: results repeat bit for bit.
+// otherwise the fp32 sums are stored, and q4_sum_kernel adds them up in the order of the
+// ranges: results repeat bit for bit.
 //
 // RT = 2: a warp reads every X fragment once for two row tiles.  With one (twice the warps),
 // up_proj M = 24 took 21.5 against 20.4 us, large M = 16 48.0 against 45.5, and one token 1 to
@@ -327,7 +327,6 @@ struct Q4Params {
   Q4View w;
   uint16_t* Y;
   float* part;      // [2 CTAs][M][128]: a CTA's range has at most two blocks it shares
-  uint32_t* count;  // [blocks][8 row tiles] arrivals, zero between calls
   int* status;
   int M, R;
   int fail;         // failure tests only: the first CTA leaves out one copy of X
@@ -434,7 +433,7 @@ __device__ __forceinline__ void q4_consume(const Q4Params& p, uint8_t* smem, Q4C
   using L = Q4Layout<NT>;
   constexpr int RT = L::RT;
   constexpr int kRecord = 64 * kQ4Cols + kQ4Cols / GROUP * (ZEROS ? 384 : 256);  // bytes
-  const int cta = blockIdx.x, ctas = gridDim.x;
+  const int cta = blockIdx.x;
   const int g = lane >> 2, tl = lane & 3, tk = q4_token(g);
   // X comes after the kernel ahead: the bounded waits below do not run while that one does
   if (p.R == 0) griddep_wait();
@@ -510,8 +509,7 @@ __device__ __forceinline__ void q4_consume(const Q4Params& p, uint8_t* smem, Q4C
     if (q4_aborted(ctrl)) return;  // the values are not whole: nothing of the block is written
     // this warp's rows of the block: values (row, token) at 4 places of each 16 x 8 tile
     const size_t n0 = static_cast<size_t>(block) * 128;
-    int place = 0;
-    auto each = [&](auto&& f, int& j) {
+    auto each = [&](auto&& f) {
 #pragma unroll
       for (int r = 0; r < RT; ++r)
 #pragma unroll
@@ -519,7 +517,6 @@ __device__ __forceinline__ void q4_consume(const Q4Params& p, uint8_t* smem, Q4C
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int m = 8 * k + tl + 4 * (e & 1), row = (warp * RT + r) * 16 + g + 8 * (e >> 1);
-            j = (r * NT + k) * 4 + e;
             if (m < p.M) f(acc[r][k][e], m, row);
           }
     };
@@ -527,45 +524,11 @@ __device__ __forceinline__ void q4_consume(const Q4Params& p, uint8_t* smem, Q4C
       reinterpret_cast<__nv_bfloat16*>(p.Y)[static_cast<size_t>(m) * p.w.N + n0 + row] = __float2bfloat16_rn(v);
     };
     if (n == p.records) {
-      each(store, place);
+      each(store);
     } else {
-      const size_t slot = static_cast<size_t>(p.M) * 128;
       // a block that the range starts in takes the CTA's slot 0, one that it ends in slot 1
-      float* mine = p.part + (2 * static_cast<size_t>(cta) + (i == i0 ? 0 : 1)) * slot;
-      each([&](float v, int m, int row) { __stcg(mine + m * 128 + row, v); }, place);
-      __threadfence();
-      __syncwarp();
-      const long long b0 = static_cast<long long>(block) * p.records;
-      const int f = q4_owner(p.total, b0, ctas), l = q4_owner(p.total, b0 + p.records - 1, ctas);
-      uint32_t last = 0;
-      if (lane == 0) last = atomicAdd(p.count + block * 8 + warp, 1u) == static_cast<uint32_t>(l - f);
-      if (__shfl_sync(0xffffffffu, last, 0)) {
-        __threadfence();
-        // the first CTA of the block has it in slot 1 unless its range starts with the block
-        const float* from = p.part + (2 * static_cast<size_t>(f) + (q4_range(p.total, f, ctas) == b0 ? 0 : 1)) * slot;
-        each([&](float& v, int m, int row) { v = __ldcg(from + m * 128 + row); }, place);
-        const float* next = p.part + 2 * static_cast<size_t>(f + 1) * slot;
-        int c = f + 1;
-        // the values of several ranges at once: one trip to L2 for all of them
-        constexpr int kAtOnce = NT <= 2 ? 4 : 1;
-        for (; c + kAtOnce <= l + 1; c += kAtOnce, next += 2 * kAtOnce * slot) {
-          float v[kAtOnce][RT * NT * 4];
-#pragma unroll
-          for (int k = 0; k < kAtOnce; ++k) {
-            int j = 0;
-            each([&](float&, int m, int row) { v[k][j] = __ldcg(next + 2 * k * slot + m * 128 + row); }, j);
-          }
-#pragma unroll
-          for (int k = 0; k < kAtOnce; ++k) {
-            int j = 0;
-            each([&](float& a, int, int) { a += v[k][j]; }, j);
-          }
-        }
-        for (; c <= l; ++c, next += 2 * slot)
-          each([&](float& v, int m, int row) { v += __ldcg(next + m * 128 + row); }, place);
-        each(store, place);
-        if (lane == 0) p.count[block * 8 + warp] = 0u;
-      }
+      float* mine = p.part + (2 * static_cast<size_t>(cta) + (i == i0 ? 0 : 1)) * (static_cast<size_t>(p.M) * 128);
+      each([&](float v, int m, int row) { __stcg(mine + m * 128 + row, v); });
     }
     i += n;
   }
@@ -690,6 +653,40 @@ __global__ void __launch_bounds__(Q4Layout<NT>::kThreads, Q4Layout<NT>::kPerSm)
     q4_consume<NT, GROUP, ZEROS>(p, smem, ctrl, i0, i1, ranks, warp, lane);
   }
   if (p.parts > 1) q4_join<NT>(p, smem, ctrl, static_cast<int>(i0 / p.records));
+}
+
+// The sums of the row blocks that lie in several ranges, added up in the order of the ranges,
+// into Y: CTA x takes block x, a warp a token, a lane 4 rows.  A launch of its own, which
+// starts with the layer kernel and waits for it: nothing is counted or reset, so the calls on
+// a weight share no state.
+struct Q4SumParams {
+  const float* part;  // as in Q4Params
+  uint16_t* Y;
+  int M, N, records, ctas;
+  long long total;
+};
+constexpr int kQ4SumWarps = 4;
+
+__global__ void __launch_bounds__(32 * kQ4SumWarps) q4_sum_kernel(const __grid_constant__ Q4SumParams p) {
+  griddep_launch_dependents();  // a kernel launched to overlap this one waits for it itself
+  const int block = blockIdx.x, m = blockIdx.y * kQ4SumWarps + (threadIdx.x >> 5), row = (threadIdx.x & 31) * 4;
+  const long long b0 = static_cast<long long>(block) * p.records;
+  const int f = q4_owner(p.total, b0, p.ctas), l = q4_owner(p.total, b0 + p.records - 1, p.ctas);
+  griddep_wait();  // in every CTA: this grid ends after the layer kernel
+  if (f == l || m >= p.M) return;
+  const size_t slot = static_cast<size_t>(p.M) * 128;
+  const float* at = p.part + static_cast<size_t>(m) * 128 + row;
+  // the first CTA of the block has it in slot 1 unless its range starts with the block
+  float4 v = __ldcg(reinterpret_cast<const float4*>(
+      at + (2 * static_cast<size_t>(f) + (q4_range(p.total, f, p.ctas) == b0 ? 0 : 1)) * slot));
+#pragma unroll 4
+  for (int c = f + 1; c <= l; ++c) {
+    const float4 x = __ldcg(reinterpret_cast<const float4*>(at + 2 * static_cast<size_t>(c) * slot));
+    v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+  }
+  const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
+  *reinterpret_cast<uint2*>(p.Y + static_cast<size_t>(m) * p.N + block * 128 + row) =
+      make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
 }
 
 // ------------------------------------------------------------------------------------
