@@ -342,7 +342,9 @@ __global__ void __launch_bounds__(kGradThreads, BN == 256 ? 1 : 2)
         const int row = r0 + i / quads, c = i % quads * 4;
         const bool live = p0 + row < p.P;
         const size_t pr = static_cast<size_t>(p0) + row;
-        float4 v = load4(row, c);
+        // ranks past R are held as zeros: their sums are of zeros, or NaN where an operand is
+        // infinite, and a NaN would reach the whole row of dX
+        float4 v = c < p.R ? load4(row, c) : make_float4(0.f, 0.f, 0.f, 0.f);
         if (p.mode == GRAD_SPLIT) {
           const uint32_t h0 = pack(v.x, v.y), h1 = pack(v.z, v.w);
           if (live) {
