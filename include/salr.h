@@ -402,7 +402,8 @@ SALR_API int salr_q4_encode(const void* W, int64_t N, int64_t K, int64_t group, 
  * Arithmetic: products of bf16 values accumulate in fp32 on the tensor cores; dY B_cat^T and
  * X A_cat are kept as two bf16 parts (16 bits of significand); a 4-bit weight enters as the
  * bf16 rounding that salr_decode gives.  Each output is rounded once, and results repeat
- * bit for bit.
+ * bit for bit.  Infinities in dY and X give those of the formulas; an infinite value of A_cat
+ * may give NaN in dX where the formula gives an infinity (it meets both parts of dY B_cat^T).
  *
  * One to four kernels (and a memset where tiles of dX are split), with scratch from the library's pool taken on `stream`
  * and given back to it in stream order: with dX the dense weight (2 N K bytes), and 8 to 16

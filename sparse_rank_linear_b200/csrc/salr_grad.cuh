@@ -322,12 +322,15 @@ __global__ void __launch_bounds__(kGradThreads, BN == 256 ? 1 : 2)
       const float h0 = __uint_as_float(h << 16), h1 = __uint_as_float(h & 0xffff0000u);
       return pack(fabsf(h0) <= 3.402823466e38f ? a - h0 : 0.f, fabsf(h1) <= 3.402823466e38f ? b - h1 : 0.f);
     };
+    // The sums with hi and lo together.  One with hi that is infinite stands alone: it came from
+    // an infinite X or dY, whose product with lo is NaN (lo = 0) or may have the other sign.
+    auto whole = [](float hi, float lo) { return fabsf(hi) <= 3.402823466e38f ? hi + lo : hi; };
     if (p.mode == GRAD_COLS) {  // lanes down the rows, which are neighbours in the output
       for (int i = tid; i < rows * (p.R / 4); i += 128) {
         const int row = r0 + i % rows, c = i / rows * 4;
         float4 v = load4(row, c);
         const float4 w = load4(row, p.half + c);
-        v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
+        v = make_float4(whole(v.x, w.x), whole(v.y, w.y), whole(v.z, w.z), whole(v.w, w.w));
         if (p0 + row < p.P) {
           __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(p.out) + static_cast<size_t>(c) * p.ldo + p0 + row;
           o[0] = __float2bfloat16_rn(v.x);
@@ -354,7 +357,7 @@ __global__ void __launch_bounds__(kGradThreads, BN == 256 ? 1 : 2)
           }
         } else {
           const float4 w = load4(row, p.half + c);
-          v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
+          v = make_float4(whole(v.x, w.x), whole(v.y, w.y), whole(v.z, w.z), whole(v.w, w.w));
           if (live) *reinterpret_cast<uint2*>(p.out + pr * p.R + c) = make_uint2(pack(v.x, v.y), pack(v.z, v.w));
         }
       }

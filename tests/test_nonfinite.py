@@ -49,3 +49,18 @@ def test_infinite_gradient_of_the_result_in_dX(kind, R, sign):
     dY[9, 5] = sign * INF
     dX = salr.linear_backward(dY, X, w, A, B, needs=(True, False, False))[0]
     same(dX, product(dY, W) + product(product(dY, B.t()), A.t()))
+
+
+@gpu
+@pytest.mark.parametrize("R", [8, 64, 72, 128])
+@pytest.mark.parametrize("place", ["dY", "X"])
+def test_infinite_inputs_in_dA_and_dB(R, place):
+    w, W, X, dY, A, B = setup(70, R, "q4", False)
+    if place == "dY":
+        dY[9, 5], dY[33, 100] = INF, -INF
+    else:
+        X[9, 5], X[33, 100] = INF, -INF
+    _, dA, dB = salr.linear_backward(dY, X, w, A, B, needs=(False, True, True))
+    u, t = product(dY, B.t()), product(X, A)
+    same(dA, product(X.t(), u))
+    same(dB, product(t.t(), dY))
