@@ -1381,6 +1381,7 @@ int salr_linear(const void* X, int64_t M, salr_handle h, const void* A_cat, cons
     tp.counters = t.counters;
     tp.status = h->status;
     tp.M = static_cast<int>(M);
+    tp.R = static_cast<int>(R);
     tp.R16 = R16;
     tp.kblocks = KB;
     tp.TT = TT;

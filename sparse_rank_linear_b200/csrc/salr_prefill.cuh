@@ -660,7 +660,7 @@ struct TParams {
   float* T32;          // [tokens x 128 ranks] fp32 sums of K splits (token-major), zero between calls
   uint32_t* counters;  // [TT x 4] split arrivals per token tile and 32-rank quarter
   int* status;
-  int M, R16, kblocks, TT, splits;
+  int M, R, R16, kblocks, TT, splits;
 };
 
 struct TCtrl {
@@ -763,6 +763,8 @@ __global__ void __launch_bounds__(kTThreads, 1)
     const int q = warp & 3;
     const uint32_t lane_base = static_cast<uint32_t>(32 * q) << 16;
     const int r = 32 * q + lane;
+    // ranks R .. R16 - 1 are zeros, not their sums, which are NaN where X is infinite
+    const bool real = r < p.R;
     bool ok = mbar_wait(&ctrl->fin, 0) && !*abort_flag;
     ok = __all_sync(0xffffffffu, ok);
     if (ok) {
@@ -778,7 +780,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
           if (r < p.R16) {
 #pragma unroll
             for (int e = 0; e < 16; ++e)
-              if (c + e < mvalid) T[(row0 + c + e) * 128 + r] = __float2bfloat16_rn(__uint_as_float(v[e]));
+              if (c + e < mvalid) T[(row0 + c + e) * 128 + r] = __float2bfloat16_rn(real ? __uint_as_float(v[e]) : 0.f);
           }
         }
       } else {
@@ -810,7 +812,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
 #pragma unroll
               for (int e = 0; e < 32; ++e)
                 if (c0 + e < mvalid) {
-                  T[(row0 + c0 + e) * 128 + r] = __float2bfloat16_rn(tv[e]);
+                  T[(row0 + c0 + e) * 128 + r] = __float2bfloat16_rn(real ? tv[e] : 0.f);
                   __stcg(sum + (c0 + e) * 128, 0.f);
                 }
             }

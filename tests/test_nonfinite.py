@@ -64,3 +64,12 @@ def test_infinite_inputs_in_dA_and_dB(R, place):
     u, t = product(dY, B.t()), product(X, A)
     same(dA, product(X.t(), u))
     same(dB, product(t.t(), dY))
+
+
+@gpu
+@pytest.mark.parametrize("M", [4, 70, 300])
+@pytest.mark.parametrize("R", [8, 16, 24, 40, 128])
+def test_infinite_activation_over_a_4_bit_weight(M, R):
+    w, W, X, _, A, B = setup(M, R, "q4", True)
+    X[2, 7] = INF
+    same(salr.linear(X, w, A, B), product(X, W.t()) + product(product(X, A), B))
