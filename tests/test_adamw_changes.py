@@ -1,0 +1,47 @@
+"""AdamW between steps: gradients of another shape or type."""
+import pytest
+import torch
+
+import sparse_rank_linear_b200 as salr
+
+gpu = pytest.mark.gpu
+
+
+def zeros(*shape, dtype=torch.float32):
+    return torch.zeros(*shape, device="cuda", dtype=dtype)
+
+
+@gpu
+@pytest.mark.parametrize("grad", [(6, 4), (24,), (4, 6, 1), (2, 12)])
+def test_gradient_of_another_shape_is_refused(grad):
+    p = [zeros(4, 6), zeros(3)]
+    opt = salr.AdamW(p)
+    ok = [torch.ones(4, 6, device="cuda"), torch.ones(3, device="cuda")]
+    for other in (ok[1], None):
+        with pytest.raises(ValueError, match="grads"):
+            opt.step([torch.ones(grad, device="cuda"), other])
+    opt.step(ok)
+    with pytest.raises(ValueError, match="grads"):  # after a step too
+        opt.step([torch.ones(grad, device="cuda"), ok[1]])
+    opt.step(ok)
+    assert opt.step_count.item() == 2
+
+
+@gpu
+def test_gradients_may_change_type_and_be_left_out_between_steps():
+    p = [zeros(4, 6), zeros(3)]
+    opt = salr.AdamW(p, lr=0.1, weight_decay=0.0)
+    g = [torch.ones(4, 6, device="cuda"), torch.ones(3, device="cuda")]
+    opt.step(g)
+    opt.step([x.bfloat16() for x in g])
+    opt.step([None, g[1]])
+    opt.step(g)
+    with pytest.raises(TypeError):
+        opt.step([g[0], g[1].bfloat16()])
+    with pytest.raises(TypeError):
+        opt.step([x.half() for x in g])
+    with pytest.raises(ValueError):
+        opt.step([x.cpu() for x in g])
+    assert opt.step_count.item() == 4
+    # m / sqrt(v) is 1 in every step, but that the first tensor's moments miss one
+    assert ((p[1] + 0.4).abs() < 1e-5).all() and (p[0] < -0.25).all() and (p[0] == p[0][0, 0]).all()
