@@ -120,7 +120,7 @@ class AdamW:
                 self._master[s].copy_(p.detach().reshape(-1))
         self._step = torch.zeros(2, dtype=torch.int64, device=self.device)
         self._shapes = [p.shape for p in self.params]
-        self._grads_seen = _Watch()
+        self._grads_seen, self._params_seen = _Watch(), _Watch()
         self._table = (AdamwTensor * len(self.params))()
         for t, p, s in zip(self._table, self.params, self.slices):
             t.exp_avg = m.data_ptr() + s.start * m.element_size()
@@ -190,14 +190,16 @@ class AdamW:
                 self._grads_seen.learn(grads)
             some = iter(some)
             pointers = [0 if g is None else next(some) for g in grads]
-        # the parameters may have moved since the last step (p.data = ...)
+        # the parameters may have moved since the last step, or be another view of their
+        # memory (p.data = ...)
         at = list(map(torch.Tensor.data_ptr, self.params))
-        if at != self._at:
+        if at != self._at or not self._params_seen.same(self.params):
             at, now = self._pointers(self.params, self._shapes, "params")
             if now != self._kind:
                 raise TypeError("params must keep their type")
             self._at = at
             self._params[:] = at
+            self._params_seen.learn(self.params)
             # kept alive: while they are, an unchanged address means unchanged memory
             self._kept = [p.detach() for p in self.params]
         self._grads[:] = pointers

@@ -1,4 +1,4 @@
-"""AdamW between steps: gradients of another shape or type."""
+"""AdamW between steps: gradients of another shape or type, and parameters whose view changed."""
 import pytest
 import torch
 
@@ -45,3 +45,39 @@ def test_gradients_may_change_type_and_be_left_out_between_steps():
     assert opt.step_count.item() == 4
     # m / sqrt(v) is 1 in every step, but that the first tensor's moments miss one
     assert ((p[1] + 0.4).abs() < 1e-5).all() and (p[0] < -0.25).all() and (p[0] == p[0][0, 0]).all()
+
+
+@gpu
+def test_parameter_that_became_transposed_in_place_is_refused():
+    p = zeros(4, 4)
+    opt = salr.AdamW([p])
+    g = torch.ones(4, 4, device="cuda")
+    opt.step([g])
+    p.data = p.data.t()
+    with pytest.raises(ValueError, match="params"):
+        opt.step([g])
+    p.data = p.data.t()
+    opt.step([g])
+    assert opt.step_count.item() == 2
+
+
+@gpu
+def test_parameter_of_another_type_in_place_is_refused():
+    p = zeros(40, dtype=torch.bfloat16)
+    opt = salr.AdamW([p])
+    g = torch.ones(40, device="cuda")
+    opt.step([g])
+    p.data = p.data.view(torch.float16)
+    with pytest.raises(TypeError, match="params"):
+        opt.step([g])
+
+
+@gpu
+def test_parameter_that_became_shorter_in_place_is_refused():
+    p = zeros(300)
+    opt = salr.AdamW([p])
+    g = torch.ones(300, device="cuda")
+    opt.step([g])
+    p.data = p.data[:299]
+    with pytest.raises(ValueError, match="params"):
+        opt.step([g])
