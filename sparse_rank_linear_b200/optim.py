@@ -85,10 +85,7 @@ class AdamW:
                 raise ValueError(f"params[{i}] must be a CUDA tensor")
             if p.device != first.device:
                 raise ValueError("params must be on one device")
-        spans = sorted((p.data_ptr(), p.data_ptr() + p.numel() * p.element_size())
-                       for p in self.params if p.numel())
-        if any(a[1] > b[0] for a, b in zip(spans, spans[1:])):
-            raise ValueError("params must not overlap (the same tensor twice?)")
+        self._refuse_overlap()
         if state_bits not in (8, 32):
             raise ValueError("state_bits must be 8 or 32")
         if master and first.dtype != torch.bfloat16:
@@ -163,6 +160,12 @@ class AdamW:
             raise ValueError(f"{what} must be contiguous, of the parameters' shapes and on {self.device}")
         return pointers, kind
 
+    def _refuse_overlap(self):
+        spans = sorted((p.data_ptr(), p.data_ptr() + p.numel() * p.element_size())
+                       for p in self.params if p.numel())
+        if any(a[1] > b[0] for a, b in zip(spans, spans[1:])):
+            raise ValueError("params must not overlap (the same tensor twice?)")
+
     def _scalar(self, x, name):
         import torch
         if x.dtype != torch.float32 or x.numel() != 1 or x.device != self.device:
@@ -171,7 +174,8 @@ class AdamW:
 
     def step(self, grads, lr=None, grad_scale=None, stream=None):
         """One step with ``grads``, one contiguous tensor of the parameter's shape (all of one
-        type, bfloat16 or float32) or None per parameter; None leaves its parameter and moments as they are.
+        type, bfloat16 or float32) or None per parameter; None leaves its parameter and
+        moments as they are.
 
         ``lr``: a number or a one-element float32 CUDA tensor in place of ``self.lr``.
         ``grad_scale``: a one-element float32 CUDA tensor that multiplies every gradient (the
@@ -197,6 +201,7 @@ class AdamW:
             at, now = self._pointers(self.params, self._shapes, "params")
             if now != self._kind:
                 raise TypeError("params must keep their type")
+            self._refuse_overlap()
             self._at = at
             self._params[:] = at
             self._params_seen.learn(self.params)

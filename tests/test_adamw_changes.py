@@ -81,3 +81,18 @@ def test_parameter_that_became_shorter_in_place_is_refused():
     p.data = p.data[:299]
     with pytest.raises(ValueError, match="params"):
         opt.step([g])
+
+
+@gpu
+def test_parameters_that_moved_onto_one_another_are_refused():
+    p = [zeros(30), zeros(30)]
+    opt = salr.AdamW(p)
+    g = [torch.ones(30, device="cuda") for _ in p]
+    opt.step(g)
+    both = zeros(60)
+    p[0].data, p[1].data = both[:30], both[20:50]
+    with pytest.raises(ValueError, match="overlap"):
+        opt.step(g)
+    p[1].data = both[30:]
+    opt.step(g)
+    assert opt.step_count.item() == 2
