@@ -62,6 +62,9 @@ class AdamW:
     * ``exp_avg_scale``, ``exp_avg_sq_scale``: the codes' scales (None with 32 bits);
     * ``master``: fp32 (None without); ``step_count``: int64 scalar, the steps done.
 
+    ``lr``, ``betas``, ``eps`` and ``weight_decay`` are attributes that the next step takes as
+    they are then (the library refuses values outside their ranges).
+
     Steps are stream-ordered and allocate nothing, so a step can be captured into a CUDA
     graph: a replay takes the step count, and ``lr`` and ``grad_scale`` given as tensors, as
     they are then.
@@ -134,9 +137,8 @@ class AdamW:
         self._params = words[:, AdamwTensor.param.offset // 8]
         self._index = self._step.get_device()
         self._at = None  # the parameters' addresses in the table
-        self._config = AdamwConfig(beta1=beta1, beta2=beta2, eps=eps, step=self._step.data_ptr(),
-                                   param_type=_TYPES[str(first.dtype)], state_bits=state_bits,
-                                   master=1 if master else 0)
+        self._config = AdamwConfig(step=self._step.data_ptr(), param_type=_TYPES[str(first.dtype)],
+                                   state_bits=state_bits, master=1 if master else 0)
 
     exp_avg = _held("_exp_avg")
     exp_avg_sq = _held("_exp_avg_sq")
@@ -217,7 +219,8 @@ class AdamW:
             c.lr_dev = self._scalar(lr, "lr")
         else:
             c.lr = lr
-        c.weight_decay = self.weight_decay
+        c.beta1, c.beta2 = self.betas
+        c.eps, c.weight_decay = self.eps, self.weight_decay
         c.grad_scale = None if grad_scale is None else self._scalar(grad_scale, "grad_scale")
         with _on_device(self._step):
             _check("salr_adamw", load_library().salr_adamw(self._table, len(self._table), ctypes.byref(c),

@@ -1,4 +1,5 @@
-"""AdamW between steps: gradients of another shape or type, and parameters whose view changed."""
+"""AdamW between steps: gradients of another shape or type, parameters whose view changed, and
+attributes that are set."""
 import pytest
 import torch
 
@@ -96,3 +97,29 @@ def test_parameters_that_moved_onto_one_another_are_refused():
     p[1].data = both[30:]
     opt.step(g)
     assert opt.step_count.item() == 2
+
+
+@gpu
+@pytest.mark.parametrize("bits", [32, 8])
+def test_eps_and_betas_take_effect_when_set(bits):
+    g = torch.Generator(device="cuda").manual_seed(0)
+    start = torch.randn(500, generator=g, device="cuda")
+    grad = torch.randn(500, generator=g, device="cuda") * 1e-3
+    got = []
+    for given in (True, False):
+        p = start.clone()
+        kw = dict(betas=(0.5, 0.75), eps=1e-3) if given else {}
+        opt = salr.AdamW([p], lr=0.1, state_bits=bits, **kw)
+        if not given:
+            opt.betas, opt.eps = (0.5, 0.75), 1e-3
+        for _ in range(3):
+            opt.step([grad])
+        got.append(p)
+    assert torch.equal(*got)
+    for name, bad in (("betas", (1.0, 0.9)), ("betas", (0.9, -0.1)), ("eps", -1.0), ("eps", float("nan"))):
+        good = getattr(opt, name)
+        setattr(opt, name, bad)
+        with pytest.raises(salr.SalrError, match="INVALID"):
+            opt.step([grad])
+        setattr(opt, name, good)
+    assert opt.step_count.item() == 3
