@@ -148,6 +148,13 @@ def _require(t, name, shape=None, device=True, beside=None):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
+def _written(tensors):
+    """Tell autograd that the library wrote into tensors of the caller's: a graph that saved one
+    of them then refuses its backward pass, as after torch's own in-place operations."""
+    import torch
+    torch.autograd.graph.increment_version(tensors)
+
+
 class Weight:
     """An encoded weight (pruned and bitmap-stored, or 4-bit codes with group scales): owns
     a ``salr_handle``."""
@@ -191,10 +198,13 @@ class Weight:
     def decode(self, out=None, stream=None):
         import torch
         inf = self.info()
-        if out is None:
+        given = out is not None
+        if not given:
             out = torch.empty(inf["N"], inf["K"], dtype=torch.bfloat16, device="cuda")
         _require(out, "W_out", (inf["N"], inf["K"]))
         _check("salr_decode", load_library().salr_decode(self.handle, _ptr(out), _stream_ptr(stream)))
+        if given:
+            _written((out,))
         return out
 
     def to_bytes(self, stream=None) -> bytes:
@@ -326,7 +336,8 @@ def residual_adapter(W, weight: Weight, r: int, q: int = 2, oversample: int = 16
 def linear(X, weight: Weight, A_cat=None, B_cat=None, Y=None, stream=None):
     """salr_linear: Y = X (M.W)^T + (X A_cat) B_cat; returns Y (M x N bf16).  Calls on one
     bitmap weight share workspace that it holds, so they must not run at the same time on
-    different streams; calls on one 4-bit weight may."""
+    different streams; calls on one 4-bit weight may.  No call of this module is recorded for
+    autograd: ``linear_backward`` gives the gradients."""
     N, K = weight._shape()
     _require(X, "X")
     M = X.shape[0]
@@ -337,13 +348,16 @@ def linear(X, weight: Weight, A_cat=None, B_cat=None, Y=None, stream=None):
         R = A_cat.shape[1]
         _require(A_cat, "A_cat", (K, R), beside=X)
         _require(B_cat, "B_cat", (R, N), beside=X)
-    if Y is None:
+    given = Y is not None
+    if not given:
         Y = X.new_empty((M, N))
     else:
         _require(Y, "Y", (M, N), beside=X)
     with _on_device(X):
         _check("salr_linear", load_library().salr_linear(
             _ptr(X), M, weight.handle, _ptr(A_cat), _ptr(B_cat), R, _ptr(Y), _stream_ptr(stream)))
+    if given:
+        _written((Y,))
     return Y
 
 
@@ -371,7 +385,7 @@ def linear_backward(dY, X, weight: Weight, A_cat=None, B_cat=None, dX=None, dA=N
         _require(X, "X", (M, K), beside=dY)
     else:
         X = None
-    out = []
+    out, given = [], []
     for want, t, name, shape in ((want_x, dX, "dX", (M, K)), (want_a, dA, "dA", (K, R)),
                                  (want_b, dB, "dB", (R, N))):
         if not want:
@@ -380,12 +394,15 @@ def linear_backward(dY, X, weight: Weight, A_cat=None, B_cat=None, dX=None, dA=N
             t = dY.new_empty(shape)
         else:
             _require(t, name, shape, beside=dY)
+            given.append(t)
         out.append(t)
     dX, dA, dB = out
     with _on_device(dY):
         _check("salr_linear_backward", load_library().salr_linear_backward(
             _ptr(dY), _ptr(X), M, weight.handle, _ptr(A_cat), _ptr(B_cat), R, _ptr(dX), _ptr(dA),
             _ptr(dB), _stream_ptr(stream)))
+    if given:
+        _written(given)
     return dX, dA, dB
 
 
@@ -398,6 +415,7 @@ def linear_host(X_host, weight: Weight, A_cat, B_cat, Y_host, stream=None):
     _check("salr_linear_host", load_library().salr_linear_host(
         _ptr(X_host), X_host.shape[0], weight.handle, _ptr(A_cat), _ptr(B_cat), R, _ptr(Y_host),
         _stream_ptr(stream)))
+    _written((Y_host,))
     return Y_host
 
 

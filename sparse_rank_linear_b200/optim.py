@@ -11,7 +11,7 @@ import math
 
 import numpy as np
 
-from .binding import AdamwConfig, AdamwTensor, _check, _on_device, _stream_ptr, load_library
+from .binding import AdamwConfig, AdamwTensor, _check, _on_device, _stream_ptr, _written, load_library
 
 BLOCK = 256  # elements that share a scale of the 8-bit moments
 _TYPES = {"torch.bfloat16": 0, "torch.float32": 1}
@@ -186,6 +186,7 @@ class AdamW:
         grads = list(grads)
         if len(grads) != len(self.params):
             raise ValueError(f"{len(grads)} gradients for {len(self.params)} params")
+        changed = self.params
         if self._grads_seen.same(grads):
             pointers, kind = list(map(torch.Tensor.data_ptr, grads)), grads[0].dtype
         else:
@@ -194,6 +195,8 @@ class AdamW:
             some, kind = self._pointers(given, shapes, "grads")
             if len(given) == len(grads):
                 self._grads_seen.learn(grads)
+            else:
+                changed = [p for p, g in zip(self.params, grads) if g is not None]
             some = iter(some)
             pointers = [0 if g is None else next(some) for g in grads]
         # the parameters may have moved since the last step, or be another view of their
@@ -225,3 +228,4 @@ class AdamW:
         with _on_device(self._step):
             _check("salr_adamw", load_library().salr_adamw(self._table, len(self._table), ctypes.byref(c),
                                                            _stream_ptr(stream)))
+        _written(changed)

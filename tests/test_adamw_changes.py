@@ -1,5 +1,5 @@
-"""AdamW between steps: gradients of another shape or type, parameters whose view changed, and
-attributes that are set."""
+"""AdamW between steps: gradients of another shape, parameters whose view changed, attributes
+that are set, and what autograd learns of a step."""
 import pytest
 import torch
 
@@ -123,3 +123,43 @@ def test_eps_and_betas_take_effect_when_set(bits):
             opt.step([grad])
         setattr(opt, name, good)
     assert opt.step_count.item() == 3
+
+
+@gpu
+def test_autograd_learns_that_a_step_changed_the_parameters():
+    p = torch.ones(8, device="cuda", requires_grad=True)
+    q = torch.ones(8, device="cuda", requires_grad=True)
+    y, z = (p * p).sum(), (q * q).sum()  # both save their factors
+    opt = salr.AdamW([p, q])
+    opt.step([torch.ones(8, device="cuda"), None])
+    z.backward()  # q was left alone
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward()
+
+
+@gpu
+def test_decode_and_host_results_count_as_written():
+    g = torch.Generator(device="cuda").manual_seed(0)
+    w = salr.encode_q4(torch.randn(128, 128, generator=g, device="cuda").bfloat16(), 64)
+    out = torch.empty(128, 128, device="cuda", dtype=torch.bfloat16)
+    host = torch.zeros(4, 128, dtype=torch.bfloat16).pin_memory()
+    there = torch.empty(4, 128, dtype=torch.bfloat16).pin_memory()
+    w.decode(out)
+    salr.linear_host(host, w, None, None, there)
+    torch.cuda.synchronize()
+    assert out._version == 1 and there._version == 1 and host._version == 0
+
+
+@gpu
+def test_autograd_learns_that_results_were_written_into_a_tensor():
+    g = torch.Generator(device="cuda").manual_seed(0)
+    W = torch.randn(128, 128, generator=g, device="cuda").bfloat16()
+    X = torch.randn(4, 128, generator=g, device="cuda").bfloat16()
+    w = salr.encode_q4(W, 64)
+    a = torch.ones(4, 128, device="cuda", dtype=torch.bfloat16, requires_grad=True)
+    for write in (lambda y: salr.linear(X, w, Y=y), lambda y: salr.linear_backward(X, X, w, dX=y)):
+        buffer = torch.ones(4, 128, device="cuda", dtype=torch.bfloat16)
+        s = (a * buffer).sum()  # saves the buffer
+        write(buffer)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            s.backward()
