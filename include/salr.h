@@ -412,7 +412,8 @@ SALR_API int salr_q4_encode(const void* W, int64_t N, int64_t K, int64_t group, 
  * as the graph's own.
  *
  * SALR_ERR_INVALID: a bad handle or one of another device, a NULL dY, all outputs NULL, dA
- * or dB with R == 0 or a NULL X, R > 0 with a NULL adapter, M < 1, R < 0.
+ * or dB with R == 0 or a NULL X, R > 0 with a NULL adapter, M < 1, R < 0, an output that
+ * overlaps another argument that the call reads or writes.
  * SALR_ERR_UNSUPPORTED: M, R or alignment outside the shape rules.
  */
 SALR_API int salr_linear_backward(const void* dY, const void* X, int64_t M, salr_handle h,

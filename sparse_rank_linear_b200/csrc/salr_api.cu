@@ -1719,6 +1719,11 @@ int salr_linear_backward(const void* dY, const void* X, int64_t M64, salr_handle
       (R64 > 0 && (!aligned16(A_cat) || !aligned16(B_cat))))
     return SALR_ERR_UNSUPPORTED;
   if (!on_current_device(h)) return SALR_ERR_INVALID;
+  const size_t tokens = 2 * static_cast<size_t>(M64), ranks = 2 * static_cast<size_t>(R64);
+  if (outputs_overlap<7>({{dX, tokens * h->K}, {dA, ranks * h->K}, {dB, ranks * h->N}, {dY, tokens * h->N},
+                          {dA || dB ? X : nullptr, tokens * h->K}, {R64 > 0 ? A_cat : nullptr, ranks * h->K},
+                          {R64 > 0 ? B_cat : nullptr, ranks * h->N}}, 3))
+    return SALR_ERR_INVALID;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int M = static_cast<int>(M64), N = static_cast<int>(h->N), K = static_cast<int>(h->K);
   const int R = static_cast<int>(R64), half = R <= 64 ? 64 : 128;

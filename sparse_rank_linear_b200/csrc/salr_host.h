@@ -3,6 +3,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <cstddef>
 #include <cstdint>
 
 #include "../../include/salr.h"
@@ -10,6 +11,23 @@
 namespace salr {
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+struct Span {  // memory of an argument; NULL: not given
+  const void* at;
+  size_t bytes;
+};
+inline bool overlap(const Span& a, const Span& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.at), y = reinterpret_cast<uintptr_t>(b.at);
+  return a.at && b.at && x < y + b.bytes && y < x + a.bytes;
+}
+// Whether a written argument (the first `outputs` of `spans`) overlaps another one.
+template <size_t N>
+bool outputs_overlap(const Span (&spans)[N], size_t outputs) {
+  for (size_t i = 0; i < outputs; ++i)
+    for (size_t j = i + 1; j < N; ++j)
+      if (overlap(spans[i], spans[j])) return true;
+  return false;
+}
 
 inline int cuda_status(cudaError_t e) {
   if (e == cudaSuccess) return SALR_OK;

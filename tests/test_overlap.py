@@ -1,0 +1,40 @@
+"""Outputs that overlap what a call reads or writes are refused before anything is queued."""
+import pytest
+import torch
+
+import sparse_rank_linear_b200 as salr
+
+gpu = pytest.mark.gpu
+
+
+def flat(n):
+    return torch.randn(n, device="cuda").bfloat16()
+
+
+@gpu
+@pytest.mark.parametrize("kind", ["bitmap", "q4"])
+def test_gradients_refuse_outputs_that_overlap(kind):
+    N = K = 128
+    M, R = 16, 8
+    W = flat(N * K).view(N, K)
+    w = salr.encode(W, 0.5) if kind == "bitmap" else salr.encode_q4(W, 64)
+    dY, X, A, B = flat(M * N).view(M, N), flat(M * K).view(M, K), flat(K * R).view(K, R), flat(R * N).view(R, N)
+    pool = flat(M * K + 64)
+    first, second = pool[:M * K].view(M, K), pool[64:].view(M, K)
+    small = pool[64:64 + K * R]
+    kept = [t.clone() for t in (dY, X, A, B, pool)]
+    for out in (dict(dX=dY), dict(dX=X), dict(dA=A), dict(dB=B), dict(dA=B.view(K, R)), dict(dB=A.view(R, N)),
+                dict(dX=first, dA=small.view(K, R)), dict(dX=first, dB=small.view(R, N)),
+                dict(dA=pool[:K * R].view(K, R), dB=small.view(R, N))):
+        with pytest.raises(salr.SalrError, match="INVALID"):
+            salr.linear_backward(dY, X, w, A, B, **out)
+    with pytest.raises(salr.SalrError, match="INVALID"):  # by one row's end
+        salr.linear_backward(first, X, w, dX=second, needs=(True, False, False))
+    assert all(torch.equal(a, b) for a, b in zip((dY, X, A, B, pool), kept))
+    # side by side, and over an X that the call does not read
+    want = salr.linear_backward(dY, X, w, A, B)
+    both = flat(2 * K * R)
+    got = salr.linear_backward(dY, X, w, A, B, dA=both[:K * R].view(K, R), dB=both[K * R:].view(R, N))
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    over = salr.linear_backward(dY, None, w, A, B, dX=X, needs=(True, False, False))[0]
+    assert over.data_ptr() == X.data_ptr() and torch.equal(X, want[0])
