@@ -127,7 +127,8 @@ SALR_API int salr_decode(salr_handle h, void* W_out, void* stream);
  * M     number of tokens, >= 1.
  * A_cat device, K x R bf16; B_cat device, R x N bf16.  R == 0 means no adapter; the
  *       pointers are then ignored and may be NULL.
- * Y     device, M x N bf16, overwritten (no accumulation into Y).
+ * Y     device, M x N bf16, overwritten (no accumulation into Y).  A Y that overlaps an
+ *       input is refused (SALR_ERR_INVALID).
  *
  * Arithmetic: products of bf16 inputs accumulate in fp32 on the tensor cores.  The
  * adapter's inner product t = X A_cat is accumulated in fp32 and rounded once to bf16

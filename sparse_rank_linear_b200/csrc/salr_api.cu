@@ -741,6 +741,14 @@ int check_linear_args(const void* X, int64_t M, salr_handle h, const void* A, co
   return SALR_OK;
 }
 
+// Whether Y overlaps an input of the layer, other CTAs of which may still read it.
+bool output_overlaps(const void* X, int64_t M, salr_handle h, const void* A, const void* B, int64_t R,
+                     const void* Y) {
+  const size_t tokens = 2 * static_cast<size_t>(M), ranks = 2 * static_cast<size_t>(R);
+  return outputs_overlap<4>({{Y, tokens * h->N}, {X, tokens * h->K}, {R > 0 ? A : nullptr, ranks * h->K},
+                             {R > 0 ? B : nullptr, ranks * h->N}}, 1);
+}
+
 // CTAs of the layer kernel whose room a CTA of the t kernel takes.
 template <int NT>
 constexpr int q4_beside() {
@@ -1241,6 +1249,7 @@ int salr_linear(const void* X, int64_t M, salr_handle h, const void* A_cat, cons
                 int64_t R, void* Y, void* stream) {
   int rc = check_linear_args(X, M, h, A_cat, B_cat, R, Y);
   if (rc != SALR_OK) return rc;
+  if (output_overlaps(X, M, h, A_cat, B_cat, R, Y)) return SALR_ERR_INVALID;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (h->group && !on_current_device(h)) return SALR_ERR_INVALID;
   if (h->group && M <= kQ4MaxTokens) return launch_q4_linear(X, M, h, A_cat, B_cat, R, Y, st);
@@ -2144,6 +2153,7 @@ extern "C" int salr_linear_noalloc(const void* X, int64_t M, salr_handle h, cons
                                    const void* B_cat, int64_t R, void* Y, void* stream) {
   int rc = check_linear_args(X, M, h, A_cat, B_cat, R, Y);
   if (rc != SALR_OK) return rc;
+  if (output_overlaps(X, M, h, A_cat, B_cat, R, Y)) return SALR_ERR_INVALID;
   if (h->group || M > kNoAllocMaxM || h->N > kNoAllocMaxN) return SALR_ERR_UNSUPPORTED;
   int dev = 0;
   SALR_TRY(cudaGetDevice(&dev));
