@@ -155,6 +155,13 @@ def _written(tensors):
     torch.autograd.graph.increment_version(tensors)
 
 
+def _ranks(A_cat, B_cat):
+    """The adapters' rank, 0 without."""
+    if (A_cat is None) != (B_cat is None):
+        raise ValueError("A_cat and B_cat must be given together")
+    return 0 if A_cat is None else A_cat.shape[1]
+
+
 class Weight:
     """An encoded weight (pruned and bitmap-stored, or 4-bit codes with group scales): owns
     a ``salr_handle``."""
@@ -343,9 +350,8 @@ def linear(X, weight: Weight, A_cat=None, B_cat=None, Y=None, stream=None):
     M = X.shape[0]
     if X.shape[1] != K:
         raise ValueError("X has the wrong number of columns")
-    R = 0
+    R = _ranks(A_cat, B_cat)
     if A_cat is not None:
-        R = A_cat.shape[1]
         _require(A_cat, "A_cat", (K, R), beside=X)
         _require(B_cat, "B_cat", (R, N), beside=X)
     given = Y is not None
@@ -371,9 +377,8 @@ def linear_backward(dY, X, weight: Weight, A_cat=None, B_cat=None, dX=None, dA=N
     if dY.dim() != 2 or dY.shape[1] != N:
         raise ValueError("dY has the wrong number of columns")
     M = dY.shape[0]
-    R = 0
+    R = _ranks(A_cat, B_cat)
     if A_cat is not None:
-        R = A_cat.shape[1]
         _require(A_cat, "A_cat", (K, R), beside=dY)
         _require(B_cat, "B_cat", (R, N), beside=dY)
     want_x, want_a, want_b = bool(needs[0]), bool(needs[1]) and R > 0, bool(needs[2]) and R > 0
@@ -411,7 +416,7 @@ def linear_host(X_host, weight: Weight, A_cat, B_cat, Y_host, stream=None):
     inf = weight.info()
     _require(X_host, "X_host", device=False)
     _require(Y_host, "Y_host", (X_host.shape[0], inf["N"]), device=False)
-    R = 0 if A_cat is None else A_cat.shape[1]
+    R = _ranks(A_cat, B_cat)
     _check("salr_linear_host", load_library().salr_linear_host(
         _ptr(X_host), X_host.shape[0], weight.handle, _ptr(A_cat), _ptr(B_cat), R, _ptr(Y_host),
         _stream_ptr(stream)))
