@@ -457,7 +457,7 @@ SALR_API int salr_linear_backward(const void* dY, const void* X, int64_t M, salr
  *   grad_scale     device, one fp32, or NULL for 1.
  *
  * param and grad need the alignment of their type only; tensors whose param and grad are
- * 16-byte aligned are read by 16-byte loads.  One kernel launch per 448 tensors; nothing is
+ * 16-byte aligned are read by 16-byte loads.  One kernel launch per 480 tensors; nothing is
  * allocated or kept, so a captured step can be replayed: it then reads step, lr_dev and
  * grad_scale as they are at the replay.  Two steps over the same tensors or the same `step`
  * must be ordered on one stream.

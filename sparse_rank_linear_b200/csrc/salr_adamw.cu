@@ -13,10 +13,14 @@ using namespace salr;
 namespace {
 
 // Tables of two sizes: the parameters of a launch are copied whole, and a step over a few
-// tensors should not carry the 30 KB of a whole model's (kernel parameters end at 32764
-// bytes).
-constexpr int kFewTensors = 24, kManyTensors = 448;
-static_assert(sizeof(AdamTable<kManyTensors>) <= 32764, "kernel parameter space");
+// tensors should not carry the 32 KB of a whole model's, which is as long as the kernel
+// parameters may be.
+constexpr size_t kParameterBytes = 32764;
+constexpr int kFewTensors = 24;
+constexpr int kManyTensors = 1 + static_cast<int>((kParameterBytes - sizeof(AdamTable<1>)) /
+                                                  (sizeof(AdamTensor) + sizeof(int)));
+static_assert(sizeof(AdamTable<kManyTensors>) <= kParameterBytes, "kernel parameter space");
+static_assert(kManyTensors == 480, "salr.h gives the count");
 static_assert(sizeof(AdamTensor) == sizeof(salr_adamw_tensor), "same table entry");
 
 template <int MAXT, typename PT, typename GT, bool MASTER, bool EIGHT>
