@@ -367,7 +367,8 @@ SALR_API int salr_residual_adapter(const void* W, salr_handle h, int64_t r, cons
  * salr_linear on such a handle: for M <= 64 the codes are rebuilt in registers (q - z
  * exactly, in bf16), products and sums are fp32, each group's sum is scaled in fp32 (so a
  * group's sum of (q - z) X must stay finite before it is scaled: |X| up to 2^116 is safe), t =
- * X A_cat is kept as two bf16 parts (16 bits of significand), and results repeat bit for bit.
+ * X A_cat is kept as two bf16 parts (16 bits of significand; an infinite value of B_cat meets
+ * both, and may give NaN where the formula gives an infinity), and results repeat bit for bit.
  * One kernel, one more with adapters, and one more where row blocks are shared by CTAs whose
  * sums meet in memory.  Above that, the weight is expanded to a dense bf16 scratch (s (q - z)
  * rounded once) and the rest is as described under salr_linear.  The handle must be on the
@@ -406,9 +407,11 @@ SALR_API int salr_q4_encode(const void* W, int64_t N, int64_t K, int64_t group, 
  * bit for bit.  Infinities in dY and X give those of the formulas; an infinite value of A_cat
  * may give NaN in dX where the formula gives an infinity (it meets both parts of dY B_cat^T).
  *
- * One to four kernels (and a memset where tiles of dX are split), with scratch from the library's pool taken on `stream`
- * and given back to it in stream order: with dX the dense weight (2 N K bytes), and 8 to 16
- * bytes per token and rank.  Nothing of the handle is written but its status word, so calls
+ * One to four kernels (and a memset where tiles of dX are split), with scratch from the
+ * library's pool taken on `stream` and given back to it in stream order: with dX the dense
+ * weight (2 N K bytes); with R > 0, 512 bytes per token for R <= 64 and 1024 above; and where
+ * the dX tiles of a last round are split, their fp32 parts, 256 KiB (tiles of 256 columns) or
+ * 512 KiB (of 512) for each of 2 to 4 parts of a tile, under 74 tiles on 148 SMs.  Nothing of the handle is written but its status word, so calls
  * on one handle may run concurrently on several streams; captured, a call keeps its scratch
  * as the graph's own.
  *

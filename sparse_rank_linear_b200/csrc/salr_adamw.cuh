@@ -21,7 +21,7 @@
 // block's loads (up to 96 bytes a thread) issued before this one is worked on.  The tensor
 // table travels in the kernel's parameters: no copy, nothing to keep alive, one launch.
 // Measured over the 448 adapter tensors (238 M elements) of 32 layers: fp32 moments and master
-// copies 1.12 ms, 6.0 TB/s or 0.93 of the measured copy rate; 8-bit moments 0.61 ms, 3.9 TB/s,
+// copies 1.13 ms, 5.9 TB/s or 0.91 of the measured copy rate; 8-bit moments 0.61 ms, 4.0 TB/s,
 // where about 66 instructions an element, at 3 of 4 issue slots, are the bound.
 #pragma once
 #include <cstdint>

@@ -20,19 +20,21 @@
 //
 // Arithmetic: 0x4300 | q is bf16 128 + q; minus the bf16 128 + z it is q - z, exactly.  The
 // products q x are exact in fp32 and accumulate in fp32 over a group (64 columns of it, if it
-// is longer), which is then scaled in fp32.  t = X A is summed in fp32 and enters the adapter's product with 16 bits of
-// significand.  Y is rounded once.
+// is longer), which is then scaled in fp32.  t = X A is summed in fp32 and enters the adapter's
+// product with 16 bits of significand.  Y is rounded once.
 //
 // Bound: HBM, by the codes (0.5 byte per weight plus scales), in the limit.  At the copy rate
 // an SM has 46 weights to rebuild per cycle; the rebuild is 0.9 instructions per weight on the
 // integer pipe (half of the issue rate), at most 73 weights per cycle, and with the products,
-// the scaling and the stages' handshake measured 24 at M = 1 on 28672 x 8192 (34.1 us, 3.9
-// TB/s).  m16n8k16 takes 8 cycles per scheduler, so from about 20 tokens on the products set
-// the floor: 1024 / M weights per cycle; measured half of that (large M = 64: 121 us).  The legacy products are the choice because they take
-// the rebuilt weights from registers and give each group's sum back in registers, where its
-// fp32 scale is one multiply-add; in tensor memory, the scale would have to be rounded into
-// the bf16 weights.  Short calls are bound by latencies (launch, first copy 2 us, sums over a
-// cluster 2 us): 5.9 us for 4096 x 4096 at M = 1, its bytes' time being 1.4.
+// the scaling and the stages' handshake measured 24 at M = 1 on 28672 x 8192 (34 us, 3.9
+// TB/s).  Nothing is full there (issue slots 51%, HBM 60%): two warps a scheduler wait for
+// stages and fixed latencies.  m16n8k16 takes 8 cycles per scheduler, so from about 20 tokens on
+// the products set the floor: 1024 / M weights per cycle; measured half of that (28672 x 8192 at
+// M = 64: 98 us).  The legacy products are the choice because they take the rebuilt weights from
+// registers and give each group's sum back in registers, where its fp32 scale is one
+// multiply-add; in tensor memory, the scale would have to be rounded into the bf16 weights.
+// Short calls are bound by latencies (launch, first copy 2 us, sums over a cluster 2 us): 6.0 us
+// for 4096 x 4096 at M = 1, its bytes' time being 1.4.
 #pragma once
 #include <cstdint>
 #include <cuda_bf16.h>
@@ -302,7 +304,9 @@ __global__ void __launch_bounds__(Q4TLayout<NT>::kThreads)
 // RT = 2: a warp reads every X fragment once for two row tiles.  With one (twice the warps),
 // up_proj M = 24 took 21.5 against 20.4 us, large M = 16 48.0 against 45.5, and one token 1 to
 // 2% more.  Deep rings count for more than warps: at one token, three CTAs an SM of three
-// stages took 46.3 us on 28672 x 8192 where two of four stages take 37.2.
+// stages took 46.3 us on 28672 x 8192 where two of four stages took 37.2.  (All of these with
+// the ranges' sums added by the last warp to arrive: q4_sum_kernel brought 28672 x 8192 to 34 us
+// at M = 1, 40 at M = 16 with adapters, and from 121 to 98 at M = 64.)
 template <int NT>
 struct Q4Layout {
   static constexpr int RT = 2;
@@ -691,7 +695,10 @@ __global__ void __launch_bounds__(32 * kQ4SumWarps) q4_sum_kernel(const __grid_c
 
 // ------------------------------------------------------------------------------------
 // The dense bf16 weight [N x K] (s (q - z), rounded once), for larger token counts, the
-// gradients and salr_decode.  One warp per 16 rows x 64 columns: each lane writes whole
+// gradients and salr_decode.  s (q - z) has up to 12 bits of significand, a bf16 operand 8: the
+// rounding is that of a dense bf16 weight, half a step (2^-8) of each product at most, 0.0014 in
+// norm where Y's own rounding is 0.0017.  Kept exactly, as two operands, the weight would take
+// the tensor cores twice.  One warp per 16 rows x 64 columns: each lane writes whole
 // 16-byte pieces, four neighbouring lanes 64 consecutive bytes.
 template <int GROUP, bool ZEROS>
 __global__ void __launch_bounds__(256) q4_expand_kernel(const Q4View w, uint16_t* __restrict__ out) {
