@@ -763,8 +763,6 @@ __global__ void __launch_bounds__(kTThreads, 1)
     const int q = warp & 3;
     const uint32_t lane_base = static_cast<uint32_t>(32 * q) << 16;
     const int r = 32 * q + lane;
-    // ranks R .. R16 - 1 are zeros, not their sums, which are NaN where X is infinite
-    const bool real = r < p.R;
     bool ok = mbar_wait(&ctrl->fin, 0) && !*abort_flag;
     ok = __all_sync(0xffffffffu, ok);
     if (ok) {
@@ -772,15 +770,19 @@ __global__ void __launch_bounds__(kTThreads, 1)
       const int mvalid = min(BNT, p.M - j * BNT);
       const size_t row0 = static_cast<size_t>(j) * BNT;
       __nv_bfloat16* T = reinterpret_cast<__nv_bfloat16*>(p.T);
+      // Ranks R .. R16 - 1 are zeros, not their sums, which are NaN where X is infinite.  (In a
+      // loop of its own: a choice of value in the loops below cost down_proj M = 4096 60 us.)
+      if (r >= p.R && r < p.R16)
+        for (int c = 0; c < mvalid; ++c) T[(row0 + c) * 128 + r] = __float2bfloat16_rn(0.f);
       if (p.splits == 1) {
         for (int c = 0; c < BNT; c += 16) {
           uint32_t v[16];
           tmem_ld16(tmem + lane_base + c, v);
           tmem_ld_wait();
-          if (r < p.R16) {
+          if (r < p.R) {
 #pragma unroll
             for (int e = 0; e < 16; ++e)
-              if (c + e < mvalid) T[(row0 + c + e) * 128 + r] = __float2bfloat16_rn(real ? __uint_as_float(v[e]) : 0.f);
+              if (c + e < mvalid) T[(row0 + c + e) * 128 + r] = __float2bfloat16_rn(__uint_as_float(v[e]));
           }
         }
       } else {
@@ -791,7 +793,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
           uint32_t v[16];
           tmem_ld16(tmem + lane_base + c, v);
           tmem_ld_wait();
-          if (r < p.R16) {
+          if (r < p.R) {
 #pragma unroll
             for (int e = 0; e < 16; ++e)
               if (c + e < mvalid) red_add_f32(sum + (c + e) * 128, __uint_as_float(v[e]));
@@ -803,7 +805,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
         if (lane == 0) last = atomicAdd(p.counters + j * 4 + q, 1u) == static_cast<uint32_t>(p.splits - 1);
         if (__shfl_sync(0xffffffffu, last, 0)) {
           __threadfence();
-          if (r < p.R16) {
+          if (r < p.R) {
             // 32 tokens per L2 round trip: a chunk's loads all go out before its stores
             for (int c0 = 0; c0 < mvalid; c0 += 32) {
               float tv[32];
@@ -812,7 +814,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
 #pragma unroll
               for (int e = 0; e < 32; ++e)
                 if (c0 + e < mvalid) {
-                  T[(row0 + c0 + e) * 128 + r] = __float2bfloat16_rn(real ? tv[e] : 0.f);
+                  T[(row0 + c0 + e) * 128 + r] = __float2bfloat16_rn(tv[e]);
                   __stcg(sum + (c0 + e) * 128, 0.f);
                 }
             }
