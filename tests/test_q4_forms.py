@@ -86,3 +86,25 @@ def test_gradients_of_the_codes_own_weight(group, zeros, M):
     assert (err <= tol).all(), f"worst {(err / tol).max().item():.3f} of the tolerance"
     assert (err.norm() / want.norm()).item() <= 4e-3
     assert w.sync_status() == 0
+
+
+@gpu
+def test_calls_on_one_weight_at_a_time_with_more_tokens():
+    """Three streams over one weight, with 100, 300 and 20 tokens: each right, whatever the others do."""
+    N, K, R = 1024, 768, 40
+    codes, s, z, W, g = make(N, K, 64, True)
+    w = salr.pack_q4(codes, s, z)
+    A, B = adapters(g, N, K, R)
+    Xs = [bf16(g, m, K) for m in (100, 300, 20)]
+    want = [X.double() @ W.t() + (X.double() @ A.double()) @ B.double() for X in Xs]
+    streams = [torch.cuda.Stream() for _ in Xs]
+    torch.cuda.synchronize()
+    got = [[] for _ in Xs]
+    for _ in range(10):
+        for k, X in enumerate(Xs):
+            with torch.cuda.stream(streams[k]):
+                got[k].append(salr.linear(X, w, A, B))
+    torch.cuda.synchronize()
+    for ys, v in zip(got, want):
+        assert all((y.double() - v).norm() <= 4e-3 * v.norm() for y in ys)
+    assert w.sync_status() == 0
